@@ -1,4 +1,4 @@
-"""B200 (sm_100a) NHWC convolution forward.
+"""B200 (sm_100a) NHWC convolution forward, and the sequence operators next to conv1d.
 
 The library itself is the C-ABI shared object built from ``csrc/`` (declared in
 ``include/b200conv.h``); ``binding`` marshals arguments into it with ctypes and
@@ -14,11 +14,16 @@ _BINDING_NAMES = frozenset({
     "fp32_fma_rate",
     "conv_status_string", "conv_device_props", "conv_accumulate", "conv_profile_begin", "conv_profile_end",
     "profile_end", "KernelTime",
+    "conv1d_causal_forward", "conv1d_causal_step_forward", "selective_scan_forward", "selective_scan_step_forward",
+    "selective_scan_plan", "selective_scan_plan_for_props",
+    "selective_scan_workspace_size",
     # types and helpers
     "ConvError", "Conv1dDesc", "Conv2dDesc", "Conv3dDesc", "ConvPlan", "ConvOptions", "DeviceProps",
     "ALGO", "DTYPE", "STATUS", "ENGINE", "library_path", "make_desc2d", "make_desc3d", "make_options",
+    "CausalConvDesc", "ScanDesc", "ScanTensors", "ScanPlan", "ACTIVATION",
     # torch conveniences
     "conv1d", "conv2d", "conv3d", "plan2d", "plan3d",
+    "conv1d_causal", "conv1d_causal_step", "selective_scan", "selective_scan_step",
 })
 
 

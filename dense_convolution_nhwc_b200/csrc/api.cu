@@ -86,11 +86,13 @@ long long out_extent(long long in, int k, int s, int p, int d) {
 
 enum Kind { K_TC_CONV, K_TC_CONV3D, K_SIMT_CONV, K_SPLITK_REDUCE, K_WINO_FILTER, K_WINO_INPUT, K_WINO_GEMM_TC, K_WINO_GEMM_SIMT,
             K_WINO_OUTPUT, K_WINO3D_FILTER, K_WINO3D_INPUT, K_WINO3D_GEMM_TC, K_WINO3D_GEMM_SIMT, K_WINO3D_OUTPUT,
-            K_ACCUMULATE, K_CHANNEL_PAD, K_FILL, K_WINO_PASS, K_WINO_FUSED, K_COUNT };
+            K_ACCUMULATE, K_CHANNEL_PAD, K_FILL, K_WINO_PASS, K_WINO_FUSED,
+            K_CAUSAL_CONV, K_CAUSAL_CONV_STEP, K_SCAN, K_SCAN_STEP, K_COUNT };
 const char* const kKindName[K_COUNT] = {"tc_conv", "tc_conv3d", "simt_conv", "splitk_reduce", "wino_filter", "wino_input", "wino_gemm_tc",
                                         "wino_gemm_simt", "wino_output", "wino3d_filter", "wino3d_input", "wino3d_gemm_tc",
                                         "wino3d_gemm_simt", "wino3d_output", "accumulate", "channel_pad", "fill",
-                                        "wino_pass", "wino_fused"};
+                                        "wino_pass", "wino_fused", "causal_conv", "causal_conv_step", "selective_scan",
+                                        "selective_scan_step"};
 
 struct ProfRecord {
   int kind;
@@ -1037,6 +1039,103 @@ conv_status_t run3d_winograd(const void* in, const void* w, void* out, const Geo
 }
 
 }  // namespace
+// ---------------------------- sequence operators -------------------------------
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 30;
+
+// The memory between a tensor's first and last element.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// n x l rows of `cols` contiguous elements (packed or a single token: one of the two is 1).
+Span span_of(const void* p, long long n, long long l, const long long* stride, long long cols, int esz) {
+  if (!p || n <= 0 || l <= 0) return {nullptr, 0};
+  return {p, (size_t)((n - 1) * stride[0] + (l - 1) * stride[1] + cols) * esz};
+}
+bool meets(const Span& a, const Span& b) { return overlaps(a.p, a.bytes, b.p, b.bytes); }
+
+// Rows that are written must not overlap each other; rows that are read may (a broadcast).
+bool valid_strides(const long long* s, long long n, long long l, long long cols, bool written) {
+  if (s[0] < 0 || s[1] < 0) return false;
+  if (!written) return true;
+  if (l > 1 && s[1] < cols) return false;
+  return n <= 1 || s[0] >= (l - 1) * s[1] + cols;
+}
+
+conv_status_t check_causal(const conv1d_causal_desc_t* d, conv_dtype_t dt, bool state, bool slots) {
+  if (!d || !valid_dtype(dt)) return CONV_ERR_INVALID;
+  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->c <= 0 || d->k < 2 || d->k > 8) return CONV_ERR_INVALID;
+  if (d->activation != CONV_ACT_NONE && d->activation != CONV_ACT_SILU) return CONV_ERR_INVALID;
+  if (!state && (d->carry || slots)) return CONV_ERR_INVALID;
+  if (state && d->state_slots < (slots ? 1 : d->n)) return CONV_ERR_INVALID;
+  return CONV_OK;
+}
+
+bool multiple_of(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// steps: one token of each of n sequences (rows n, stride [0]); packed: l rows of stride [1]
+conv_status_t check_causal_tensors(const void* x, const void* w, const void* bias, const int* offsets, const void* state,
+                                   const int* slots, const void* out, const conv1d_causal_desc_t* d, conv_dtype_t dt,
+                                   bool step) {
+  const int esz = dtype_size(dt);
+  const long long n = offsets ? 1 : d->n, l = step ? 1 : d->l;
+  if (!w || (l > 0 && (!x || !out))) return CONV_ERR_INVALID;
+  for (const void* p : {x, w, bias, state, out})
+    if (!multiple_of(p, esz)) return CONV_ERR_ALIGNMENT;
+  if (!multiple_of(offsets, 4) || !multiple_of(slots, 4)) return CONV_ERR_ALIGNMENT;
+  if (!valid_strides(d->x_stride, n, l, d->c, false) || !valid_strides(d->out_stride, n, l, d->c, true))
+    return CONV_ERR_INVALID;
+  const Span o = span_of(out, n, l, d->out_stride, d->c, esz);
+  const Span st = {state, state ? (size_t)d->state_slots * (d->k - 1) * d->c * esz : 0};
+  const Span in[] = {span_of(x, n, l, d->x_stride, d->c, esz), {w, (size_t)d->c * d->k * esz},
+                     {bias, bias ? (size_t)d->c * esz : 0}, {offsets, offsets ? ((size_t)d->n + 1) * 4 : 0},
+                     {slots, slots ? (size_t)d->n * 4 : 0}};
+  for (const Span& i : in)
+    if (meets(o, i) || meets(st, i)) return CONV_ERR_INVALID;
+  return meets(o, st) ? CONV_ERR_INVALID : CONV_OK;
+}
+
+conv_status_t check_scan(const selective_scan_desc_t* d, conv_dtype_t dt) {
+  if (!d || !valid_dtype(dt)) return CONV_ERR_INVALID;
+  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->d <= 0 || d->s <= 0 || d->s > 256) return CONV_ERR_INVALID;
+  if (d->groups <= 0 || d->d % d->groups != 0) return CONV_ERR_INVALID;
+  return CONV_OK;
+}
+
+conv_status_t check_scan_tensors(const selective_scan_tensors_t* t, const selective_scan_desc_t* d, conv_dtype_t dt,
+                                 bool step, const void* workspace = nullptr, size_t workspace_bytes = 0) {
+  const int esz = dtype_size(dt);
+  const long long n = t->offsets ? 1 : d->n, l = step ? 1 : d->l, gs = (long long)d->groups * d->s;
+  if (!t->a || (l > 0 && (!t->x || !t->dt || !t->b || !t->c || !t->out))) return CONV_ERR_INVALID;
+  if (!t->state && (step || d->carry || t->slots)) return CONV_ERR_INVALID;
+  if (t->state && d->state_slots < (t->slots ? 1 : d->n)) return CONV_ERR_INVALID;
+  for (const void* p : {t->x, t->dt, t->b, t->c, t->z, (const void*)t->out})
+    if (!multiple_of(p, esz)) return CONV_ERR_ALIGNMENT;
+  for (const void* p : {(const void*)t->a, (const void*)t->d, (const void*)t->dt_bias, (const void*)t->offsets,
+                        (const void*)t->slots, (const void*)t->state})
+    if (!multiple_of(p, 4)) return CONV_ERR_ALIGNMENT;
+  if (!valid_strides(d->x_stride, n, l, d->d, false) || !valid_strides(d->dt_stride, n, l, d->d, false) ||
+      (t->z && !valid_strides(d->z_stride, n, l, d->d, false)) || !valid_strides(d->b_stride, n, l, gs, false) ||
+      !valid_strides(d->c_stride, n, l, gs, false) || !valid_strides(d->out_stride, n, l, d->d, true))
+    return CONV_ERR_INVALID;
+  const Span o = span_of(t->out, n, l, d->out_stride, d->d, esz), ws = {workspace, workspace_bytes};
+  const Span st = {t->state, t->state ? (size_t)d->state_slots * d->d * d->s * 4 : 0};
+  const size_t per_channel = (size_t)d->d * 4;
+  const Span in[] = {span_of(t->x, n, l, d->x_stride, d->d, esz), span_of(t->dt, n, l, d->dt_stride, d->d, esz),
+                     span_of(t->z, n, l, d->z_stride, d->d, esz), span_of(t->b, n, l, d->b_stride, gs, esz),
+                     span_of(t->c, n, l, d->c_stride, gs, esz), {t->a, per_channel * d->s},
+                     {t->d, t->d ? per_channel : 0}, {t->dt_bias, t->dt_bias ? per_channel : 0},
+                     {t->offsets, t->offsets ? ((size_t)d->n + 1) * 4 : 0}, {t->slots, t->slots ? (size_t)d->n * 4 : 0}};
+  for (const Span& i : in)
+    if (meets(o, i) || meets(st, i) || meets(ws, i)) return CONV_ERR_INVALID;
+  return meets(o, st) || meets(o, ws) || meets(st, ws) ? CONV_ERR_INVALID : CONV_OK;
+}
+
+}  // namespace
+
 }  // namespace b200conv
 
 using namespace b200conv;
@@ -1152,6 +1251,105 @@ conv_status_t conv1d_forward(const void* in, const void* w, void* out, const con
   conv2d_desc_t d2;
   if (!desc2d_of(desc, &d2)) return CONV_ERR_INVALID;
   return conv2d_forward(in, w, out, &d2, dtype, opts, workspace, workspace_bytes, stream);
+}
+
+conv_status_t conv1d_causal_forward(const void* x, const void* w, const void* bias, const int* offsets, void* state,
+                                    const int* slots, void* out, const conv1d_causal_desc_t* desc, conv_dtype_t dtype,
+                                    void* stream) {
+  conv_status_t st = check_causal(desc, dtype, state, slots);
+  if (st != CONV_OK) return st;
+  if (desc->n == 0) return CONV_OK;
+  st = check_causal_tensors(x, w, bias, offsets, state, slots, out, desc, dtype, false);
+  if (st != CONV_OK) return st;
+  if (log_enabled())
+    std::fprintf(stderr, "b200conv: conv1d_causal n%d l%d c%d k%d %s -> packed=%d carry=%d silu=%d\n", desc->n, desc->l,
+                 desc->c, desc->k, dtype_name(dtype), offsets != nullptr, desc->carry != 0,
+                 desc->activation == CONV_ACT_SILU);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(K_CAUSAL_CONV, s);
+  return cuda_status(launch_causal_conv(*desc, dtype, x, w, bias, offsets, state, slots, out, s));
+}
+
+conv_status_t conv1d_causal_step_forward(const void* x, const void* w, const void* bias, void* state, const int* slots, void* out,
+                                 const conv1d_causal_desc_t* desc, conv_dtype_t dtype, void* stream) {
+  conv_status_t st = check_causal(desc, dtype, state, slots);
+  if (st != CONV_OK) return st;
+  if (!state) return CONV_ERR_INVALID;
+  if (desc->n == 0) return CONV_OK;
+  st = check_causal_tensors(x, w, bias, nullptr, state, slots, out, desc, dtype, true);
+  if (st != CONV_OK) return st;
+  if (log_enabled())
+    std::fprintf(stderr, "b200conv: conv1d_causal_step n%d c%d k%d %s -> silu=%d\n", desc->n, desc->c, desc->k,
+                 dtype_name(dtype), desc->activation == CONV_ACT_SILU);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(K_CAUSAL_CONV_STEP, s);
+  return cuda_status(launch_causal_conv_step(*desc, dtype, x, w, bias, state, slots, out, s));
+}
+
+conv_status_t selective_scan_plan_for_props(const selective_scan_desc_t* desc, conv_dtype_t dtype,
+                                            const conv_device_props_t* props, selective_scan_plan_t* plan) {
+  if (!props || !plan || props->sm_count <= 0) return CONV_ERR_INVALID;
+  conv_status_t st = check_scan(desc, dtype);
+  if (st != CONV_OK) return st;
+  const ScanPlan p = plan_scan(*desc, props->sm_count);
+  *plan = selective_scan_plan_t{p.lanes, p.states_per_lane, p.chunk, p.chunks, p.workspace_bytes};
+  return CONV_OK;
+}
+
+conv_status_t selective_scan_plan(const selective_scan_desc_t* desc, conv_dtype_t dtype, int device,
+                                  selective_scan_plan_t* plan) {
+  DeviceState* d = nullptr;
+  conv_status_t st = device_state(device, &d);
+  if (st != CONV_OK) return st;
+  return selective_scan_plan_for_props(desc, dtype, &d->props, plan);
+}
+
+size_t selective_scan_workspace_size(const selective_scan_desc_t* desc, conv_dtype_t dtype, int device) {
+  selective_scan_plan_t p;
+  return selective_scan_plan(desc, dtype, device, &p) == CONV_OK ? p.workspace_bytes : 0;
+}
+
+conv_status_t selective_scan_forward(const selective_scan_tensors_t* tensors, const selective_scan_desc_t* desc,
+                                     conv_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  conv_status_t st = check_scan(desc, dtype);
+  if (st != CONV_OK) return st;
+  if (desc->n == 0) return CONV_OK;
+  if (!tensors) return CONV_ERR_INVALID;
+  st = check_scan_tensors(tensors, desc, dtype, false, workspace, workspace_bytes);
+  if (st != CONV_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CONV_ERR_CUDA;
+  DeviceState* d = nullptr;
+  st = device_state(dev, &d);
+  if (st != CONV_OK) return st;
+  const ScanPlan plan = plan_scan(*desc, d->props.sm_count);
+  if (workspace_bytes < plan.workspace_bytes || (plan.workspace_bytes > 0 && !workspace)) return CONV_ERR_WORKSPACE;
+  if (plan.workspace_bytes > 0 && !aligned256(workspace)) return CONV_ERR_ALIGNMENT;
+  if (log_enabled())
+    std::fprintf(stderr,
+                 "b200conv: selective_scan n%d l%d d%d s%d g%d %s -> packed=%d carry=%d lanes=%d states=%d chunk=%d "
+                 "chunks=%d workspace=%zu\n",
+                 desc->n, desc->l, desc->d, desc->s, desc->groups, dtype_name(dtype), tensors->offsets != nullptr,
+                 desc->carry != 0, plan.lanes, plan.states_per_lane, plan.chunk, plan.chunks, plan.workspace_bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(K_SCAN, s);
+  return cuda_status(launch_selective_scan(*desc, dtype, *tensors, plan, workspace, s));
+}
+
+conv_status_t selective_scan_step_forward(const selective_scan_tensors_t* tensors, const selective_scan_desc_t* desc,
+                                  conv_dtype_t dtype, void* stream) {
+  conv_status_t st = check_scan(desc, dtype);
+  if (st != CONV_OK) return st;
+  if (desc->n == 0) return CONV_OK;
+  if (!tensors || tensors->offsets) return CONV_ERR_INVALID;
+  st = check_scan_tensors(tensors, desc, dtype, true);
+  if (st != CONV_OK) return st;
+  if (log_enabled())
+    std::fprintf(stderr, "b200conv: selective_scan_step n%d d%d s%d g%d %s\n", desc->n, desc->d, desc->s, desc->groups,
+                 dtype_name(dtype));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(K_SCAN_STEP, s);
+  return cuda_status(launch_selective_scan_step(*desc, dtype, *tensors, s));
 }
 
 conv_status_t conv3d_plan_for_props(const conv3d_desc_t* desc, conv_dtype_t dtype, const conv_device_props_t* props,

@@ -167,6 +167,24 @@ cudaError_t launch_wino3d_input(const void* in, const Geom3& g, long long u0, lo
 cudaError_t launch_wino3d_output(const float* mbuf, const Geom3& g, long long u0, long long nu, int m,
                                  long long t_stride, conv_dtype_t out_dt, void* out, cudaStream_t s);
 
+// Sequence operators: short causal depthwise conv1d, selective scan.
+cudaError_t launch_causal_conv(const conv1d_causal_desc_t& d, conv_dtype_t dt, const void* x, const void* w,
+                               const void* bias, const int* offsets, void* state, const int* slots, void* out,
+                               cudaStream_t s);
+cudaError_t launch_causal_conv_step(const conv1d_causal_desc_t& d, conv_dtype_t dt, const void* x, const void* w,
+                                    const void* bias, void* state, const int* slots, void* out, cudaStream_t s);
+struct ScanPlan {
+  int lanes, states_per_lane;   // lanes a channel, states a lane
+  int chunk, chunks;            // tokens a chunk, chunks a sequence at most (1: not cut)
+  size_t sum_offset;            // workspace: chunk states, then the chunks' sums of delta from here
+  size_t workspace_bytes;
+};
+ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count);
+cudaError_t launch_selective_scan(const selective_scan_desc_t& d, conv_dtype_t dt, const selective_scan_tensors_t& t,
+                                  const ScanPlan& plan, void* workspace, cudaStream_t s);
+cudaError_t launch_selective_scan_step(const selective_scan_desc_t& d, conv_dtype_t dt,
+                                       const selective_scan_tensors_t& t, cudaStream_t s);
+
 // Elementwise helpers.
 cudaError_t launch_accumulate(void* out, const void* tap, size_t count, conv_dtype_t dt,
                               cudaStream_t s);

@@ -1,0 +1,555 @@
+// selective_scan.cu -- the selective state space recurrence over prompts, and
+// for one new token of every sequence.
+//
+// For channel d of a sequence, S states s, group g = d / (D / G):
+//
+//   delta_t = dt_t[d] + dt_bias[d], then log(1 + exp(delta)) with softplus
+//   h_t[s]  = exp(delta_t a[d][s]) h_{t-1}[s] + delta_t b_t[g][s] x_t[d]
+//   out_t   = (sum_s c_t[g][s] h_t[s] + D[d] x_t[d]) silu(z_t[d])
+//
+// all in fp32 whatever the io type, out rounded once.
+//
+// Prompts are bound by the exponentials: one a (token, channel, state), 16 a
+// clock and SM in the special-function units, where reading and writing a
+// token's four io values costs a quarter of that.  kLanes lanes share a channel
+// with kStates states each in registers; a block of 128 threads holds 128 / kLanes
+// channels and walks the sequence in tiles of kTile tokens staged in shared
+// memory, the next tile in flight by cp.async.  Per tile the delta and
+// delta * x of each (token, channel) are computed once, spread over the channel's
+// lanes, and the sums over states of kLanes (at least 8) tokens are reduced
+// together, so that each lane ends with the sums of its own tokens.
+//
+// A call with too few channels to fill the device cuts the sequences into
+// chunks: scan_chunk_kernel leaves each chunk's final state from zero and its
+// sum of delta in the workspace, and every chunk of scan_kernel folds those
+// before it into its first state (the decay over a chunk is exp(a sum delta)).
+// That doubles the exponentials, so it needs more than two chunks to pay.
+#include <cuda_runtime.h>
+
+#include "sequence.cuh"
+
+namespace b200conv {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kTile = 32;
+
+struct ScanArgs {
+  const void *x, *dt, *b, *c, *z;
+  const float *a, *d, *dt_bias;
+  const int *offsets, *slots;
+  float* state;
+  void* out;
+  float *ws_state, *ws_sum;    // chunked: [n][chunks][D][S] states (0: the first, j + 1: after chunk j from zero), [n][chunks][D] sums
+  int n, l, channels, states, groups, state_slots, softplus, carry;
+  long long x_s[2], dt_s[2], z_s[2], b_s[2], c_s[2], out_s[2];
+  int chunk, chunks;           // tokens a chunk (a multiple of kTile), chunks a sequence
+  int tiles;                   // channel tiles a group
+  int x_v, dt_v, z_v, b_v, c_v, out_v;   // bytes an access: 16, 8, 4, or 0 for single elements
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src));
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
+}
+
+// rows x cols elements into shared rows of `pitch` elements, by all threads.
+template <typename T, int N>
+__device__ __forceinline__ void stage_by(T* dst, int pitch, const T* src, long long stride, int rows, int cols) {
+  constexpr int E = N / sizeof(T);
+  if constexpr (E > 0) {
+    const int per = cols / E;
+    for (int i = threadIdx.x; i < rows * per; i += kThreads) {
+      const int r = i / per, q = i - r * per;
+      copy_async<N>(dst + r * pitch + q * E, src + r * stride + q * E);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void stage(T* dst, int pitch, const T* src, long long stride, int rows, int cols, int bytes) {
+  if (bytes == 16) {
+    stage_by<T, 16>(dst, pitch, src, stride, rows, cols);
+  } else if (bytes == 8) {
+    stage_by<T, 8>(dst, pitch, src, stride, rows, cols);
+  } else if (bytes == 4) {
+    stage_by<T, 4>(dst, pitch, src, stride, rows, cols);
+  } else {
+    for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
+      const int r = i / cols, q = i - r * cols;
+      dst[r * pitch + q] = src[r * stride + q];
+    }
+  }
+}
+
+template <typename T, int kStates, int kLanes>
+struct Shape {
+  static constexpr int kChannels = kThreads / kLanes;
+  static constexpr int kWide = kStates * kLanes;             // states, padded
+  static constexpr int kTogether = kLanes > 8 ? kLanes : 8;  // tokens reduced together
+  static constexpr int kOwn = kTogether / kLanes;            // of which each lane ends with
+  static constexpr int kRow = kTile + 4;                     // floats a channel of delta
+  static constexpr int kCh = kChannels * sizeof(T) >= 16 ? kChannels : 16 / sizeof(T);   // raw row pitch
+  // shared memory, in bytes
+  static constexpr int kRawX = kTile * kCh * sizeof(T);
+  static constexpr int kRawB = kTile * kWide * sizeof(T);
+  static constexpr int kStage = 3 * kRawX + 2 * kRawB;
+  static constexpr int kOut = 2 * kStage;
+  static constexpr int kDelta = kOut + kRawX;
+  static constexpr int kB = kDelta + 2 * kChannels * kRow * 4;
+  static constexpr int kBytes = kB + 2 * kTile * kWide * 4;
+};
+
+// Sequence, channel tile and tokens of a block.
+struct Where {
+  int seq, group, ch, count;   // first channel, channels
+  int lo, len;                 // packed: first row; tokens of the sequence
+  int slot;
+};
+template <int kChannels>
+__device__ __forceinline__ bool locate(const ScanArgs& p, Where* w) {
+  const int per_seq = p.tiles * p.groups;
+  w->seq = blockIdx.x / per_seq;
+  const int t = blockIdx.x - w->seq * per_seq;
+  w->group = t / p.tiles;
+  const int per_group = p.channels / p.groups, at = (t - w->group * p.tiles) * kChannels;
+  w->ch = w->group * per_group + at;
+  w->count = min(kChannels, per_group - at);
+  w->slot = slot_of(p.slots, w->seq, p.state_slots);
+  w->lo = 0;
+  w->len = p.l;
+  if (p.offsets) {
+    int hi;
+    packed_range(p.offsets, w->seq, p.l, &w->lo, &hi);
+    w->len = hi - w->lo;
+  }
+  return w->slot >= 0;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* rows_of(const ScanArgs& p, const void* base, const long long (&s)[2], const Where& w,
+                                            int col) {
+  return static_cast<const T*>(base) + (p.offsets ? 0 : w.seq * s[0]) + w.lo * s[1] + col;
+}
+
+// The sums over a channel's lanes of kCount tokens' y: at each step a lane passes on
+// one half of its tokens and adds its partner's share of the other, so that lane l
+// ends with tokens l * kOwn .. of the group in y[0 .. kOwn - 1].
+template <int kOff, int kCount, int kAll>
+__device__ __forceinline__ void reduce_lanes(float (&y)[kAll], int lane) {
+  if constexpr (kOff > 0) {
+    const bool upper = lane & kOff;
+#pragma unroll
+    for (int i = 0; i < kCount / 2; ++i) {
+      const float give = upper ? y[i] : y[i + kCount / 2];
+      const float take = upper ? y[i + kCount / 2] : y[i];
+      y[i] = take + __shfl_xor_sync(0xffffffffu, give, kOff);
+    }
+    reduce_lanes<kOff / 2, kCount / 2>(y, lane);
+  }
+}
+
+// kFull: states == kStates * kLanes.  kEnds: the chunk's final state from zero and its sum of delta, no output.
+template <typename T, int kStates, int kLanes, bool kFull, bool kEnds>
+__global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
+  using L = Shape<T, kStates, kLanes>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Where w;
+  if (!locate<L::kChannels>(p, &w)) return;
+  const int chunk = blockIdx.y, begin = chunk * p.chunk;
+  const bool last = begin + p.chunk >= w.len;
+  // a chunk without tokens has nothing to do, but for the first one's state of an empty sequence
+  if (begin >= w.len && chunk > 0) return;
+  const int end = last ? w.len : begin + p.chunk;
+  const int lane = threadIdx.x % kLanes, cl = threadIdx.x / kLanes;
+  const bool live = cl < w.count;
+  const int ch = w.ch + (live ? cl : 0);
+  const int s0 = lane * kStates, have = kFull ? kStates : min(max(p.states - s0, 0), kStates);
+
+  float a2[kStates], h[kStates];
+  const float* a = p.a + (long long)ch * p.states + s0;
+  float* cache = p.state ? p.state + ((long long)w.slot * p.channels + ch) * p.states + s0 : nullptr;
+  const long long ws_row = ((long long)w.seq * p.chunks * p.channels + ch) * p.states + s0;
+  const long long ws_step = (long long)p.channels * p.states;
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) {
+    a2[i] = i < have ? __ldg(a + i) * kLog2e : 0.0f;
+    h[i] = 0.0f;
+  }
+  if constexpr (kEnds) {
+    if (last) return;            // nothing follows it
+    if (chunk == 0 && live) {
+#pragma unroll
+      for (int i = 0; i < kStates; ++i)
+        if (i < have) p.ws_state[ws_row + i] = p.carry ? cache[i] : 0.0f;
+    }
+  } else if (p.chunks > 1 && !(chunk == 0 && last)) {
+#pragma unroll
+    for (int i = 0; i < kStates; ++i)
+      if (i < have) h[i] = p.ws_state[ws_row + i];
+    for (int j = 0; j < chunk; ++j) {
+      const float sum = p.ws_sum[((long long)w.seq * p.chunks + j) * p.channels + ch];
+#pragma unroll
+      for (int i = 0; i < kStates; ++i)
+        if (i < have) h[i] = fmaf(ex2(a2[i] * sum), h[i], p.ws_state[ws_row + (j + 1) * ws_step + i]);
+    }
+  } else if (p.carry) {
+#pragma unroll
+    for (int i = 0; i < kStates; ++i)
+      if (i < have) h[i] = cache[i];
+  }
+
+  const T* x = rows_of<T>(p, p.x, p.x_s, w, w.ch);
+  const T* dt = rows_of<T>(p, p.dt, p.dt_s, w, w.ch);
+  const T* z = p.z && !kEnds ? rows_of<T>(p, p.z, p.z_s, w, w.ch) : nullptr;
+  const T* b = rows_of<T>(p, p.b, p.b_s, w, w.group * p.states);
+  const T* c = rows_of<T>(p, p.c, p.c_s, w, w.group * p.states);
+  T* out = kEnds ? nullptr : const_cast<T*>(rows_of<T>(p, p.out, p.out_s, w, w.ch));
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.0f;
+  const float skip = !kEnds && p.d ? __ldg(p.d + ch) : 0.0f;
+
+  auto raw = [&](int stage, int which) {
+    return reinterpret_cast<T*>(smem + stage * L::kStage + (which < 3 ? which * L::kRawX : 3 * L::kRawX + (which - 3) * L::kRawB));
+  };
+  T* out_tile = reinterpret_cast<T*>(smem + L::kOut);
+  float* delta_of = reinterpret_cast<float*>(smem + L::kDelta) + cl * L::kRow;
+  float* dx_of = delta_of + L::kChannels * L::kRow;
+  float* bf = reinterpret_cast<float*>(smem + L::kB);
+  float* cf = bf + kTile * L::kWide;
+
+  auto fetch = [&](int at, int stage_at) {
+    const int rows = min(kTile, end - at);
+    stage<T>(raw(stage_at, 0), L::kCh, x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
+    stage<T>(raw(stage_at, 1), L::kCh, dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
+    if (z) stage<T>(raw(stage_at, 2), L::kCh, z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
+    stage<T>(raw(stage_at, 3), L::kWide, b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
+    if (!kEnds) stage<T>(raw(stage_at, 4), L::kWide, c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  float sum = 0.0f;            // of delta, over this lane's tokens
+  if (begin < end) fetch(begin, 0);
+  for (int at = begin, turn = 0; at < end; at += kTile, turn ^= 1) {
+    const int rows = min(kTile, end - at);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (at + kTile < end) fetch(at + kTile, turn ^ 1);
+
+    const T *xr = raw(turn, 0), *dr = raw(turn, 1), *zr = raw(turn, 2), *br = raw(turn, 3), *cr = raw(turn, 4);
+    for (int t = lane; t < rows; t += kLanes) {
+      float delta = ld_f32(dr + t * L::kCh + cl) + bias;
+      if (p.softplus) delta = softplus(delta);
+      if (!live) delta = 0.0f;
+      delta_of[t] = delta;
+      dx_of[t] = live ? delta * ld_f32(xr + t * L::kCh + cl) : 0.0f;
+      if (kEnds) sum += delta;
+    }
+    for (int i = threadIdx.x; i < rows * L::kWide; i += kThreads) {
+      const int s = i % L::kWide;
+      bf[i] = kFull || s < p.states ? ld_f32(br + i) : 0.0f;
+      if (!kEnds) cf[i] = kFull || s < p.states ? ld_f32(cr + i) : 0.0f;
+    }
+    __syncthreads();
+
+    // one token: the states advance, y is this lane's share of the sum over them
+    auto token = [&](int t, float delta, float dx) {
+      float bt[kStates], ct[kStates];
+#pragma unroll
+      for (int i = 0; i < kStates; ++i) bt[i] = bf[t * L::kWide + s0 + i];
+      if (!kEnds) {
+#pragma unroll
+        for (int i = 0; i < kStates; ++i) ct[i] = cf[t * L::kWide + s0 + i];
+      }
+      float y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kStates; ++i) {
+        if (kFull || i < have) {
+          h[i] = fmaf(ex2(a2[i] * delta), h[i], dx * bt[i]);
+          if (!kEnds) y = fmaf(ct[i], h[i], y);
+        }
+      }
+      return y;
+    };
+    for (int t = 0; t < rows; t += L::kTogether) {
+      float y[L::kTogether];
+      if (t + L::kTogether <= rows) {
+#pragma unroll
+        for (int q = 0; q < L::kTogether; q += 4) {
+          const float4 de = *reinterpret_cast<const float4*>(delta_of + t + q);
+          const float4 dx = *reinterpret_cast<const float4*>(dx_of + t + q);
+          y[q] = token(t + q, de.x, dx.x);
+          y[q + 1] = token(t + q + 1, de.y, dx.y);
+          y[q + 2] = token(t + q + 2, de.z, dx.z);
+          y[q + 3] = token(t + q + 3, de.w, dx.w);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < L::kTogether; ++q) y[q] = t + q < rows ? token(t + q, delta_of[t + q], dx_of[t + q]) : 0.0f;
+      }
+      if constexpr (!kEnds) {
+        reduce_lanes<kLanes / 2, L::kTogether>(y, lane);
+#pragma unroll
+        for (int i = 0; i < L::kOwn; ++i) {
+          const int at_t = t + lane * L::kOwn + i;
+          if (at_t < rows) {
+            float v = y[i];
+            if (p.d) v = fmaf(skip, ld_f32(xr + at_t * L::kCh + cl), v);
+            if (z) v *= silu(ld_f32(zr + at_t * L::kCh + cl));
+            st_f32(out_tile + at_t * L::kCh + cl, v);
+          }
+        }
+      }
+    }
+    if constexpr (!kEnds) {
+      __syncthreads();
+      T* to = out + at * p.out_s[1];
+      if (p.out_v == 16) {
+        constexpr int E = 16 / sizeof(T);
+        const int per = w.count / E;
+        for (int i = threadIdx.x; i < rows * per; i += kThreads) {
+          const int r = i / per, q = i - r * per;
+          *reinterpret_cast<uint4*>(to + r * p.out_s[1] + q * E) = *reinterpret_cast<const uint4*>(out_tile + r * L::kCh + q * E);
+        }
+      } else {
+        for (int i = threadIdx.x; i < rows * w.count; i += kThreads) {
+          const int r = i / w.count, q = i - r * w.count;
+          to[r * p.out_s[1] + q] = out_tile[r * L::kCh + q];
+        }
+      }
+    }
+  }
+
+  if constexpr (kEnds) {
+#pragma unroll
+    for (int off = 1; off < kLanes; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < kStates; ++i)
+      if (i < have) p.ws_state[ws_row + (chunk + 1) * ws_step + i] = h[i];
+    if (lane == 0) p.ws_sum[((long long)w.seq * p.chunks + chunk) * p.channels + ch] = sum;
+  } else if (last && live && cache) {
+#pragma unroll
+    for (int i = 0; i < kStates; ++i)
+      if (i < have) cache[i] = h[i];
+  }
+}
+
+// ------------------------------ single tokens ----------------------------------
+
+struct StepArgs {
+  const void *x, *dt, *b, *c, *z;
+  const float *a, *d, *dt_bias;
+  const int* slots;
+  float* state;
+  void* out;
+  int n, channels, states, groups, state_slots, softplus;
+  long long x_s, dt_s, z_s, b_s, c_s, out_s;
+};
+
+// Bound by the states, 8 bytes a state moved.  kLanes lanes a channel, four
+// neighbouring states a lane and turn (one 16-byte access with VEC), reduced
+// over the lanes by shuffles.
+template <typename T, int kLanes, bool VEC>
+__global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
+  const long long id = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const bool live = id < (long long)p.n * p.channels;
+  const int seq = live ? (int)(id / p.channels) : 0;
+  const int ch = live ? (int)(id - (long long)seq * p.channels) : 0;
+  const int slot = live ? slot_of(p.slots, seq, p.state_slots) : -1;
+  float y = 0.0f, xv = 0.0f;
+  if (slot >= 0) {
+    const int group = ch / (p.channels / p.groups);
+    float* state = p.state + ((long long)slot * p.channels + ch) * p.states;
+    const float* a = p.a + (long long)ch * p.states;
+    const T* b = static_cast<const T*>(p.b) + seq * p.b_s + group * p.states;
+    const T* c = static_cast<const T*>(p.c) + seq * p.c_s + group * p.states;
+    xv = ld_f32(static_cast<const T*>(p.x) + seq * p.x_s + ch);
+    float delta = ld_f32(static_cast<const T*>(p.dt) + seq * p.dt_s + ch) + (p.dt_bias ? __ldg(p.dt_bias + ch) : 0.0f);
+    if (p.softplus) delta = softplus(delta);
+    const float dx = delta * xv, de2 = delta * kLog2e;
+    for (int s = lane * 4; s < p.states; s += kLanes * 4) {
+      if constexpr (VEC) {
+        float4 h = *reinterpret_cast<const float4*>(state + s);
+        const float4 av = __ldg(reinterpret_cast<const float4*>(a + s));
+        h.x = fmaf(ex2(av.x * de2), h.x, dx * ld_f32(b + s));
+        h.y = fmaf(ex2(av.y * de2), h.y, dx * ld_f32(b + s + 1));
+        h.z = fmaf(ex2(av.z * de2), h.z, dx * ld_f32(b + s + 2));
+        h.w = fmaf(ex2(av.w * de2), h.w, dx * ld_f32(b + s + 3));
+        y = fmaf(ld_f32(c + s), h.x, y);
+        y = fmaf(ld_f32(c + s + 1), h.y, y);
+        y = fmaf(ld_f32(c + s + 2), h.z, y);
+        y = fmaf(ld_f32(c + s + 3), h.w, y);
+        *reinterpret_cast<float4*>(state + s) = h;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (s + i >= p.states) break;
+          const float h = fmaf(ex2(__ldg(a + s + i) * de2), state[s + i], dx * ld_f32(b + s + i));
+          y = fmaf(ld_f32(c + s + i), h, y);
+          state[s + i] = h;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 1; off < kLanes; off *= 2) y += __shfl_xor_sync(0xffffffffu, y, off);
+  if (slot >= 0 && lane == 0) {
+    if (p.d) y = fmaf(__ldg(p.d + ch), xv, y);
+    if (p.z) y *= silu(ld_f32(static_cast<const T*>(p.z) + seq * p.z_s + ch));
+    st_f32(static_cast<T*>(p.out) + seq * p.out_s + ch, y);
+  }
+}
+
+// -------------------------------- launches -------------------------------------
+
+// The widest access that a tensor's rows allow: base, row stride, tile width and
+// row width all multiples of it.  Copies into shared memory go down to 4 bytes.
+int access_bytes(const void* p, const long long* stride, long long cols_a, long long cols_b, int esz) {
+  for (int v = 16; v >= 4; v /= 2) {
+    if (reinterpret_cast<uintptr_t>(p) % v == 0 && stride[0] * esz % v == 0 && stride[1] * esz % v == 0 &&
+        cols_a * esz % v == 0 && cols_b * esz % v == 0)
+      return v;
+  }
+  return 0;
+}
+
+template <typename T, int kStates, int kLanes, bool kFull>
+cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
+  using L = Shape<T, kStates, kLanes>;
+  const int per_group = p.channels / p.groups, esz = sizeof(T);
+  p.tiles = (per_group + L::kChannels - 1) / L::kChannels;
+  const long long part = L::kChannels;
+  p.x_v = access_bytes(p.x, p.x_s, per_group, part, esz);
+  p.dt_v = access_bytes(p.dt, p.dt_s, per_group, part, esz);
+  p.z_v = access_bytes(p.z, p.z_s, per_group, part, esz);
+  p.b_v = access_bytes(p.b, p.b_s, p.states, p.states, esz);
+  p.c_v = access_bytes(p.c, p.c_s, p.states, p.states, esz);
+  p.out_v = access_bytes(p.out, p.out_s, per_group, part, esz);
+  const long long blocks = (long long)p.n * p.groups * p.tiles;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)p.chunks);
+  auto run = [&](auto kernel) {
+    if (L::kBytes > 48 * 1024) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+      if (e != cudaSuccess) return e;
+    }
+    kernel<<<grid, kThreads, L::kBytes, s>>>(p);
+    return cudaGetLastError();
+  };
+  if (p.chunks > 1) {
+    cudaError_t e = run(scan_kernel<T, kStates, kLanes, kFull, true>);
+    if (e != cudaSuccess) return e;
+  }
+  return run(scan_kernel<T, kStates, kLanes, kFull, false>);
+}
+
+template <typename T>
+cudaError_t scan_typed(const ScanArgs& p, const ScanPlan& plan, cudaStream_t s) {
+#define B200CONV_SCAN(S, L, F) \
+  if (plan.states_per_lane == S && plan.lanes == L && (!F || p.states == S * L)) return scan_shaped<T, S, L, F>(p, s)
+  B200CONV_SCAN(2, 8, true);
+  B200CONV_SCAN(4, 2, false);
+  B200CONV_SCAN(4, 4, false);
+  B200CONV_SCAN(4, 8, false);
+  B200CONV_SCAN(4, 16, false);
+  B200CONV_SCAN(4, 32, false);
+  B200CONV_SCAN(8, 32, false);
+#undef B200CONV_SCAN
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t step_typed(const StepArgs& p, cudaStream_t s) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.state) | reinterpret_cast<uintptr_t>(p.a)) & 15) == 0 && p.states % 4 == 0;
+  int lanes = 1;
+  while (lanes * 4 < p.states && lanes < 32) lanes *= 2;
+  const long long blocks = ((long long)p.n * p.channels * lanes + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  auto run = [&](auto kernel) {
+    kernel<<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  };
+  switch (lanes) {
+    case 1: return vec ? run(scan_step_kernel<T, 1, true>) : run(scan_step_kernel<T, 1, false>);
+    case 2: return vec ? run(scan_step_kernel<T, 2, true>) : run(scan_step_kernel<T, 2, false>);
+    case 4: return vec ? run(scan_step_kernel<T, 4, true>) : run(scan_step_kernel<T, 4, false>);
+    case 8: return vec ? run(scan_step_kernel<T, 8, true>) : run(scan_step_kernel<T, 8, false>);
+    case 16: return vec ? run(scan_step_kernel<T, 16, true>) : run(scan_step_kernel<T, 16, false>);
+    default: return vec ? run(scan_step_kernel<T, 32, true>) : run(scan_step_kernel<T, 32, false>);
+  }
+}
+
+}  // namespace
+
+// Pure in the descriptor and the device's SM count.
+ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
+  ScanPlan plan{};
+  plan.states_per_lane = 4;
+  plan.lanes = 2;
+  while (plan.lanes * plan.states_per_lane < d.s) {
+    if (plan.lanes < 32) plan.lanes *= 2;
+    else plan.states_per_lane *= 2;
+  }
+  if (d.s == 16) {
+    plan.states_per_lane = 2;
+    plan.lanes = 8;
+  }
+  const int channels = kThreads / plan.lanes;
+  const long long per_group = d.d / d.groups;
+  const long long blocks = (long long)d.n * d.groups * ((per_group + channels - 1) / channels);
+  plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
+  plan.chunks = 1;
+  // With chunks every token is gone over twice, so three are the fewest that can pay.
+  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kTile - 1) / (2 * kTile);
+  const long long chunks = want < most ? want : most;
+  if (chunks >= 4) {
+    plan.chunk = (int)(((d.l + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
+    plan.chunks = (d.l + plan.chunk - 1) / plan.chunk;
+  }
+  if (plan.chunks > 1) {
+    const size_t rows = (size_t)d.n * plan.chunks * d.d;
+    plan.sum_offset = (rows * d.s * sizeof(float) + 255) & ~size_t(255);
+    plan.workspace_bytes = plan.sum_offset + ((rows * sizeof(float) + 255) & ~size_t(255));
+  }
+  return plan;
+}
+
+cudaError_t launch_selective_scan(const selective_scan_desc_t& d, conv_dtype_t dt, const selective_scan_tensors_t& t,
+                                  const ScanPlan& plan, void* workspace, cudaStream_t s) {
+  ScanArgs p{};
+  p.x = t.x; p.dt = t.dt; p.b = t.b; p.c = t.c; p.z = t.z; p.a = t.a; p.d = t.d; p.dt_bias = t.dt_bias;
+  p.offsets = t.offsets; p.slots = t.slots; p.state = t.state; p.out = t.out;
+  p.n = d.n; p.l = d.l; p.channels = d.d; p.states = d.s; p.groups = d.groups; p.state_slots = d.state_slots;
+  p.softplus = d.softplus; p.carry = d.carry && t.state;
+  for (int i = 0; i < 2; ++i) {
+    p.x_s[i] = d.x_stride[i]; p.dt_s[i] = d.dt_stride[i]; p.z_s[i] = d.z_stride[i];
+    p.b_s[i] = d.b_stride[i]; p.c_s[i] = d.c_stride[i]; p.out_s[i] = d.out_stride[i];
+  }
+  p.chunk = plan.chunk; p.chunks = plan.chunks;
+  p.ws_state = static_cast<float*>(workspace);
+  p.ws_sum = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.sum_offset);
+  switch (dt) {
+    case CONV_F16: return scan_typed<__half>(p, plan, s);
+    case CONV_BF16: return scan_typed<__nv_bfloat16>(p, plan, s);
+    default: return scan_typed<float>(p, plan, s);
+  }
+}
+
+cudaError_t launch_selective_scan_step(const selective_scan_desc_t& d, conv_dtype_t dt, const selective_scan_tensors_t& t,
+                                       cudaStream_t s) {
+  StepArgs p{};
+  p.x = t.x; p.dt = t.dt; p.b = t.b; p.c = t.c; p.z = t.z; p.a = t.a; p.d = t.d; p.dt_bias = t.dt_bias;
+  p.slots = t.slots; p.state = t.state; p.out = t.out;
+  p.n = d.n; p.channels = d.d; p.states = d.s; p.groups = d.groups; p.state_slots = d.state_slots; p.softplus = d.softplus;
+  p.x_s = d.x_stride[0]; p.dt_s = d.dt_stride[0]; p.z_s = d.z_stride[0];
+  p.b_s = d.b_stride[0]; p.c_s = d.c_stride[0]; p.out_s = d.out_stride[0];
+  switch (dt) {
+    case CONV_F16: return step_typed<__half>(p, s);
+    case CONV_BF16: return step_typed<__nv_bfloat16>(p, s);
+    default: return step_typed<float>(p, s);
+  }
+}
+
+}  // namespace b200conv

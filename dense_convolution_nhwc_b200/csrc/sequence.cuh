@@ -1,0 +1,101 @@
+// sequence.cuh -- what the sequence operators (causal conv1d, selective scan)
+// share: where a call's sequences lie, vector loads of any alignment, and the
+// logistic functions in fp32.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace b200conv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Row range of sequence `seq` in a packed call.  Offsets come from device memory
+// and are not trusted: both ends are clamped to [0, rows], so a bad list gives
+// unspecified rows and never an access outside the tensors.
+__device__ __forceinline__ void packed_range(const int* offsets, int seq, int rows, int* lo, int* hi) {
+  const int a = min(max(__ldg(offsets + seq), 0), rows);
+  const int b = min(max(__ldg(offsets + seq + 1), a), rows);
+  *lo = a;
+  *hi = b;
+}
+
+// The cache slot of sequence `seq`, or -1 for a sequence to leave out.
+__device__ __forceinline__ int slot_of(const int* slots, int seq, int state_slots) {
+  if (!slots) return seq;
+  const int v = __ldg(slots + seq);
+  return (unsigned)v < (unsigned)state_slots ? v : -1;
+}
+
+// V elements as fp32.  VEC: one aligned access of V * sizeof(T) bytes (16 at
+// most); else V accesses of one element.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void load_f32(const T* p, float (&v)[V]) {
+  if constexpr (VEC && V * sizeof(T) == 16) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = Store<T>::to_f32(e[i]);
+  } else if constexpr (VEC && V * sizeof(T) == 8) {
+    const uint2 raw = *reinterpret_cast<const uint2*>(p);
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = Store<T>::to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = Store<T>::to_f32(p[i]);
+  }
+}
+
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
+  if constexpr (VEC && sizeof(T) == 2 && V == 8) {
+    uint4 raw;
+    raw.x = pack2<T>(v[0], v[1]);
+    raw.y = pack2<T>(v[2], v[3]);
+    raw.z = pack2<T>(v[4], v[5]);
+    raw.w = pack2<T>(v[6], v[7]);
+    *reinterpret_cast<uint4*>(p) = raw;
+  } else if constexpr (VEC && sizeof(T) == 4 && V == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = Store<T>::from_f32(v[i]);
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// v / (1 + exp(-v)).  exp(-v) overflows to infinity for v < -88 and the result
+// is then -0, the limit's nearest fp32 value; -inf gives NaN as the quotient does.
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.0f + ex2(-kLog2e * v)); }
+
+// log(1 + exp(v)) = max(v, 0) + log1p(t), t = exp(-|v|) in (0, 1].  A logarithm of
+// 1 + t would lose t's low bits where the result is small (v << 0, the usual
+// case), so log1p(t) = 2 artanh(s), s = t / (2 + t) <= 1/3, by the series
+// 2 s (1 + s^2/3 + ... + s^14/15), whose next term is below 2^-30 relative.
+__device__ __forceinline__ float softplus(float v) {
+  const float t = ex2(-kLog2e * fabsf(v));
+  const float s = t * rcp(2.0f + t);
+  const float q = s * s;
+  float p = fmaf(q, 1.0f / 15, 1.0f / 13);
+  p = fmaf(q, p, 1.0f / 11);
+  p = fmaf(q, p, 1.0f / 9);
+  p = fmaf(q, p, 1.0f / 7);
+  p = fmaf(q, p, 1.0f / 5);
+  p = fmaf(q, p, 1.0f / 3);
+  p = fmaf(q, p, 1.0f);
+  // fmaxf drops a NaN; t carries it
+  return fmaf(2.0f * s, p, fmaxf(v, 0.0f));
+}
+
+}  // namespace b200conv

@@ -1,8 +1,8 @@
 /*
  * b200conv.h -- C ABI of the B200 (sm_100a) NHWC convolution forward library.
  *
- * The operation (all entry points): a cross-correlation with zero padding,
- * groups = 1,
+ * The operation of the conv1d/2d/3d entry points: a cross-correlation with zero
+ * padding, groups = 1,
  *
  *   out[n,oh,ow,o] = sum_{kh,kw,c} in[n, oh*sh - ph + kh*dh, ow*sw - pw + kw*dw, c] * w[o,kh,kw,c]
  *   OH = floor((H + 2*ph - dh*(KH-1) - 1) / sh) + 1            (same for OW)
@@ -222,6 +222,106 @@ B200CONV_API conv_status_t conv1d_forward(const void *in, const void *w, void *o
                                           const conv1d_desc_t *desc, conv_dtype_t dtype,
                                           const conv_options_t *opts,
                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The sequence operators: the short causal depthwise convolution and the
+ * selective scan of a state-space block, over whole prompts (*_forward) and
+ * for one new token of every sequence (*_step_forward).  What they share:
+ *  - A prompt call is a dense batch (offsets NULL: n sequences of l tokens,
+ *    {batch, token} strides) or packed (offsets: n + 1 ascending int32 on the
+ *    device; sequence i is rows offsets[i] .. offsets[i+1] - 1 of l rows, the
+ *    batch stride is not read).  Sequences may be empty.  Rows outside every
+ *    sequence are neither read nor written.  Offsets are clamped to [0, l]: a
+ *    bad list gives unspecified results, never an access outside the tensors.
+ *  - Strides are in elements; the channels of a row are contiguous.  Any
+ *    alignment is accepted; 16-byte aligned bases, strides and widths run
+ *    fastest.  Pointers must be multiples of their element size, else
+ *    CONV_ERR_ALIGNMENT.
+ *  - State lives in a cache of state_slots slots owned by the caller and is
+ *    updated in place.  Sequence i uses slot slots[i] (int32 on the device), or
+ *    slot i when slots is NULL.  A sequence whose slot is outside the cache (-1,
+ *    say) is left out: nothing of it is read or written.  The slots of one call
+ *    must differ from each other; where two are equal, what that slot holds
+ *    afterwards is unspecified.
+ *  - carry != 0: each sequence continues from its slot.  carry == 0: each
+ *    starts from zero (whatever its slot holds) and leaves its state there.  For
+ *    a mix, clear the slots of the new sequences and carry.  state may be NULL
+ *    when carry is 0 and slots is NULL: nothing is kept.  A step always carries.
+ *  - At most 2^30 tokens a sequence or packed call.  out and state must not
+ *    overlap each other or any input (CONV_ERR_INVALID); the spans between a
+ *    tensor's first and last element are compared.
+ * Inputs and out are of `dtype` (weights and bias of the convolution too);
+ * arithmetic and the scan's state are fp32, each output rounded once.
+ */
+typedef enum { CONV_ACT_NONE = 0, CONV_ACT_SILU = 1 /* v / (1 + exp(-v)) */ } conv_activation_t;
+
+typedef struct {
+    int n, l, c, k;                       /* l: tokens a sequence (packed: rows); taps 2 <= k <= 8 */
+    conv_activation_t activation;
+    int carry, state_slots;
+    long long x_stride[2], out_stride[2]; /* {batch, token}; a step reads [0] alone */
+} conv1d_causal_desc_t;
+
+/*
+ * out_t[c] = act(bias[c] + sum_{j<k} w[c,j] * x_{t-(k-1)+j}[c]) for every token t
+ * of every sequence (w [C, K], the last tap on the token itself; bias [C] or
+ * NULL), accumulated in ascending j.  The k-1 tokens before a sequence's first
+ * come from state [state_slots, k-1, C] (oldest first) or are zero, and the
+ * sequence's last k-1 tokens are left there.
+ */
+B200CONV_API conv_status_t conv1d_causal_forward(const void *x, const void *w, const void *bias, const int *offsets,
+                                                 void *state, const int *slots, void *out,
+                                                 const conv1d_causal_desc_t *desc, conv_dtype_t dtype, void *stream);
+/* The same for one token of each of n sequences: x and out [N, C], the window shifted in place. */
+B200CONV_API conv_status_t conv1d_causal_step_forward(const void *x, const void *w, const void *bias, void *state,
+                                              const int *slots, void *out, const conv1d_causal_desc_t *desc,
+                                              conv_dtype_t dtype, void *stream);
+
+typedef struct {
+    int n, l, d, s, groups;               /* channels d, states 1 <= s <= 256, groups divides d */
+    int softplus, carry, state_slots;
+    long long x_stride[2], dt_stride[2], z_stride[2], b_stride[2], c_stride[2], out_stride[2];
+} selective_scan_desc_t;
+
+typedef struct {
+    const void *x, *dt;                   /* [N, L, D] */
+    const void *b, *c;                    /* [N, L, G, S], a token's G*S values contiguous */
+    const void *z;                        /* gate [N, L, D], or NULL */
+    const float *a;                       /* [D, S] */
+    const float *d, *dt_bias;             /* [D], or NULL */
+    const int *offsets, *slots;
+    float *state;                         /* [state_slots, D, S] */
+    void *out;                            /* [N, L, D] */
+} selective_scan_tensors_t;
+
+/* How a selective_scan_forward runs. */
+typedef struct {
+    int lanes, states_per_lane;           /* threads a channel, states a thread */
+    int chunk_tokens, chunks;             /* chunks > 1: each sequence is cut into up to this many
+                                             chunks that run side by side (two passes) */
+    size_t workspace_bytes;               /* bytes selective_scan_forward needs */
+} selective_scan_plan_t;
+
+/*
+ * For channel d of group g = d / (D / G), with delta_t = dt_t[d] + dt_bias[d], then
+ * log(1 + exp(delta_t)) if softplus:
+ *   h_t[s] = exp(delta_t * a[d,s]) * h_{t-1}[s] + delta_t * b_t[g,s] * x_t[d]
+ *   out_t[d] = (sum_s c_t[g,s] * h_t[s] + D[d] * x_t[d]) * silu(z_t[d])
+ * h before the first token is the slot's state (carry) or zero, and h of the
+ * last token is left there.  The plan is a pure function of the descriptor's
+ * sizes and the device's properties; the workspace rules are conv2d_forward's.
+ */
+B200CONV_API conv_status_t selective_scan_plan(const selective_scan_desc_t *desc, conv_dtype_t dtype, int device,
+                                               selective_scan_plan_t *plan);
+B200CONV_API conv_status_t selective_scan_plan_for_props(const selective_scan_desc_t *desc, conv_dtype_t dtype,
+                                                         const conv_device_props_t *props, selective_scan_plan_t *plan);
+B200CONV_API size_t selective_scan_workspace_size(const selective_scan_desc_t *desc, conv_dtype_t dtype, int device);
+B200CONV_API conv_status_t selective_scan_forward(const selective_scan_tensors_t *tensors,
+                                                  const selective_scan_desc_t *desc, conv_dtype_t dtype,
+                                                  void *workspace, size_t workspace_bytes, void *stream);
+/* The same for one token of each of n sequences: x, dt, z, out [N, D], b, c [N, G, S], strides [0] alone. */
+B200CONV_API conv_status_t selective_scan_step_forward(const selective_scan_tensors_t *tensors,
+                                               const selective_scan_desc_t *desc, conv_dtype_t dtype, void *stream);
 
 /*
  * conv3d, in[N,D,H,W,C], w[O,KD,KH,KW,C], out[N,OD,OH,OW,O].  Three algorithms:
