@@ -13,7 +13,7 @@
 // clock and SM in the special-function units, where reading and writing a
 // token's four io values costs a quarter of that.  kLanes lanes share a channel
 // with kStates states each in registers; a block of 128 threads holds 128 / kLanes
-// channels and walks the sequence in tiles of kTile tokens staged in shared
+// channels and walks the sequence in tiles of 64 tokens staged in shared
 // memory, the next tile in flight by cp.async.  Per tile the delta and
 // delta * x of each (token, channel) are computed once, spread over the channel's
 // lanes, and the sums over states of kLanes (at least 8) tokens are reduced
@@ -32,7 +32,6 @@ namespace b200conv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 32;
 
 struct ScanArgs {
   const void *x, *dt, *b, *c, *z;
@@ -43,7 +42,7 @@ struct ScanArgs {
   float *ws_state, *ws_sum;    // chunked: [n][chunks][D][S] states (0: the first, j + 1: after chunk j from zero), [n][chunks][D] sums
   int n, l, channels, states, groups, state_slots, softplus, carry;
   long long x_s[2], dt_s[2], z_s[2], b_s[2], c_s[2], out_s[2];
-  int chunk, chunks;           // tokens a chunk (a multiple of kTile), chunks a sequence
+  int chunk, chunks;           // tokens a chunk (a multiple of 64), chunks a sequence
   int tiles;                   // channel tiles a group
   int x_v, dt_v, z_v, b_v, c_v, out_v;   // bytes an access: 16, 8, 4, or 0 for single elements
 };
@@ -55,30 +54,30 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
 }
 
-// rows x cols elements into shared rows of `pitch` elements, by all threads.
-template <typename T, int N>
-__device__ __forceinline__ void stage_by(T* dst, int pitch, const T* src, long long stride, int rows, int cols) {
-  constexpr int E = N / sizeof(T);
-  if constexpr (E > 0) {
-    const int per = cols / E;
-    for (int i = threadIdx.x; i < rows * per; i += kThreads) {
-      const int r = i / per, q = i - r * per;
-      copy_async<N>(dst + r * pitch + q * E, src + r * stride + q * E);
+// rows x cols elements (cols <= kCols) into shared rows kPitch elements apart, by
+// all threads; `bytes` an access, cols and every address multiples of it.
+template <typename T, int kCols, int kPitch, int N>
+__device__ __forceinline__ void stage_by(T* dst, const T* src, long long stride, int rows, int cols) {
+  constexpr int E = N / sizeof(T), kPer = kCols / E;
+  if constexpr (E > 0 && kPer > 0) {
+    for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
+      const int r = i / kPer, q = (i % kPer) * E;
+      if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void stage(T* dst, int pitch, const T* src, long long stride, int rows, int cols, int bytes) {
+template <typename T, int kCols, int kPitch>
+__device__ __forceinline__ void stage(T* dst, const T* src, long long stride, int rows, int cols, int bytes) {
   if (bytes == 16) {
-    stage_by<T, 16>(dst, pitch, src, stride, rows, cols);
+    stage_by<T, kCols, kPitch, 16>(dst, src, stride, rows, cols);
   } else if (bytes == 8) {
-    stage_by<T, 8>(dst, pitch, src, stride, rows, cols);
+    stage_by<T, kCols, kPitch, 8>(dst, src, stride, rows, cols);
   } else if (bytes == 4) {
-    stage_by<T, 4>(dst, pitch, src, stride, rows, cols);
+    stage_by<T, kCols, kPitch, 4>(dst, src, stride, rows, cols);
   } else {
-    for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
-      const int r = i / cols, q = i - r * cols;
-      dst[r * pitch + q] = src[r * stride + q];
+    for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
+      const int r = i / kCols, q = i % kCols;
+      if (q < cols) dst[r * kPitch + q] = src[r * stride + q];
     }
   }
 }
@@ -87,18 +86,20 @@ template <typename T, int kStates, int kLanes>
 struct Shape {
   static constexpr int kChannels = kThreads / kLanes;
   static constexpr int kWide = kStates * kLanes;             // states, padded
+  static constexpr int kTile = kWide <= 32 ? 64 : 32;        // tokens staged together
   static constexpr int kTogether = kLanes > 8 ? kLanes : 8;  // tokens reduced together
   static constexpr int kOwn = kTogether / kLanes;            // of which each lane ends with
-  static constexpr int kRow = kTile + 4;                     // floats a channel of delta
-  static constexpr int kCh = kChannels * sizeof(T) >= 16 ? kChannels : 16 / sizeof(T);   // raw row pitch
+  static constexpr int kRow = kTile + 8;                     // floats a channel of delta
+  static constexpr int kPitch = kChannels + 16 / sizeof(T);  // elements a row of x: 16 bytes more, against bank conflicts
   // shared memory, in bytes
-  static constexpr int kRawX = kTile * kCh * sizeof(T);
+  static constexpr int kRawX = kTile * kPitch * sizeof(T);
   static constexpr int kRawB = kTile * kWide * sizeof(T);
   static constexpr int kStage = 3 * kRawX + 2 * kRawB;
   static constexpr int kOut = 2 * kStage;
   static constexpr int kDelta = kOut + kRawX;
   static constexpr int kB = kDelta + 2 * kChannels * kRow * 4;
   static constexpr int kBytes = kB + 2 * kTile * kWide * 4;
+  static_assert(kTile % kTogether == 0 && kStates % 2 == 0, "");
 };
 
 // Sequence, channel tile and tokens of a block.
@@ -167,14 +168,16 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
   const int ch = w.ch + (live ? cl : 0);
   const int s0 = lane * kStates, have = kFull ? kStates : min(max(p.states - s0, 0), kStates);
 
-  float a2[kStates], h[kStates];
+  float2 a2[kStates];          // a log2(e), twice
+  float h[kStates];
   const float* a = p.a + (long long)ch * p.states + s0;
   float* cache = p.state ? p.state + ((long long)w.slot * p.channels + ch) * p.states + s0 : nullptr;
   const long long ws_row = ((long long)w.seq * p.chunks * p.channels + ch) * p.states + s0;
   const long long ws_step = (long long)p.channels * p.states;
 #pragma unroll
   for (int i = 0; i < kStates; ++i) {
-    a2[i] = i < have ? __ldg(a + i) * kLog2e : 0.0f;
+    const float v = i < have ? __ldg(a + i) * kLog2e : 0.0f;
+    a2[i] = make_float2(v, v);
     h[i] = 0.0f;
   }
   if constexpr (kEnds) {
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
       const float sum = p.ws_sum[((long long)w.seq * p.chunks + j) * p.channels + ch];
 #pragma unroll
       for (int i = 0; i < kStates; ++i)
-        if (i < have) h[i] = fmaf(ex2(a2[i] * sum), h[i], p.ws_state[ws_row + (j + 1) * ws_step + i]);
+        if (i < have) h[i] = fmaf(decay(a2[i].x, sum), h[i], p.ws_state[ws_row + (j + 1) * ws_step + i]);
     }
   } else if (p.carry) {
 #pragma unroll
@@ -215,109 +218,125 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
   T* out_tile = reinterpret_cast<T*>(smem + L::kOut);
   float* delta_of = reinterpret_cast<float*>(smem + L::kDelta) + cl * L::kRow;
   float* dx_of = delta_of + L::kChannels * L::kRow;
+  // b and c in fp32, the two tokens of a pair side by side: [token / 2][state][token % 2]
   float* bf = reinterpret_cast<float*>(smem + L::kB);
-  float* cf = bf + kTile * L::kWide;
+  float* cf = bf + L::kTile * L::kWide;
 
-  auto fetch = [&](int at, int stage_at) {
-    const int rows = min(kTile, end - at);
-    stage<T>(raw(stage_at, 0), L::kCh, x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
-    stage<T>(raw(stage_at, 1), L::kCh, dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
-    if (z) stage<T>(raw(stage_at, 2), L::kCh, z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
-    stage<T>(raw(stage_at, 3), L::kWide, b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
-    if (!kEnds) stage<T>(raw(stage_at, 4), L::kWide, c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
+  auto fetch = [&](int at, int to) {
+    const int rows = min(L::kTile, end - at);
+    stage<T, L::kChannels, L::kPitch>(raw(to, 0), x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
+    stage<T, L::kChannels, L::kPitch>(raw(to, 1), dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
+    if (z) stage<T, L::kChannels, L::kPitch>(raw(to, 2), z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
+    stage<T, L::kWide, L::kWide>(raw(to, 3), b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
+    if (!kEnds) stage<T, L::kWide, L::kWide>(raw(to, 4), c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
     asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto put = [&](int at) {           // out_tile's rows, from token `at`
+    const int rows = min(L::kTile, end - at);
+    T* to = out + at * p.out_s[1];
+    constexpr int E = 16 / sizeof(T), kPer = L::kChannels / E;
+    if (kPer > 0 && p.out_v == 16) {
+      for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
+        const int r = i / (kPer > 0 ? kPer : 1), q = (i % (kPer > 0 ? kPer : 1)) * E;
+        if (q < w.count)
+          *reinterpret_cast<uint4*>(to + r * p.out_s[1] + q) = *reinterpret_cast<const uint4*>(out_tile + r * L::kPitch + q);
+      }
+    } else {
+      for (int i = threadIdx.x; i < rows * L::kChannels; i += kThreads) {
+        const int r = i / L::kChannels, q = i % L::kChannels;
+        if (q < w.count) to[r * p.out_s[1] + q] = out_tile[r * L::kPitch + q];
+      }
+    }
   };
 
   float sum = 0.0f;            // of delta, over this lane's tokens
   if (begin < end) fetch(begin, 0);
-  for (int at = begin, turn = 0; at < end; at += kTile, turn ^= 1) {
-    const int rows = min(kTile, end - at);
+  for (int at = begin, turn = 0; at < end; at += L::kTile, turn ^= 1) {
+    const int rows = min(L::kTile, end - at);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    if (at + kTile < end) fetch(at + kTile, turn ^ 1);
+    if (!kEnds && at > begin) put(at - L::kTile);
+    if (at + L::kTile < end) fetch(at + L::kTile, turn ^ 1);
 
     const T *xr = raw(turn, 0), *dr = raw(turn, 1), *zr = raw(turn, 2), *br = raw(turn, 3), *cr = raw(turn, 4);
+#pragma unroll 4
     for (int t = lane; t < rows; t += kLanes) {
-      float delta = ld_f32(dr + t * L::kCh + cl) + bias;
+      float delta = ld_f32(dr + t * L::kPitch + cl) + bias;
       if (p.softplus) delta = softplus(delta);
-      if (!live) delta = 0.0f;
       delta_of[t] = delta;
-      dx_of[t] = live ? delta * ld_f32(xr + t * L::kCh + cl) : 0.0f;
+      dx_of[t] = delta * ld_f32(xr + t * L::kPitch + cl);
       if (kEnds) sum += delta;
     }
-    for (int i = threadIdx.x; i < rows * L::kWide; i += kThreads) {
-      const int s = i % L::kWide;
-      bf[i] = kFull || s < p.states ? ld_f32(br + i) : 0.0f;
-      if (!kEnds) cf[i] = kFull || s < p.states ? ld_f32(cr + i) : 0.0f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < L::kTile / 2 * L::kWide; i += kThreads) {
+      const int s = i % L::kWide, t = i / L::kWide * 2;
+      if (t < rows) {
+        const bool real = kFull || s < p.states;
+        const T *b0 = br + t * L::kWide + s, *c0 = cr + t * L::kWide + s;
+        reinterpret_cast<float2*>(bf)[i] = real ? make_float2(ld_f32(b0), ld_f32(b0 + L::kWide)) : make_float2(0.0f, 0.0f);
+        if (!kEnds)
+          reinterpret_cast<float2*>(cf)[i] = real ? make_float2(ld_f32(c0), ld_f32(c0 + L::kWide)) : make_float2(0.0f, 0.0f);
+      }
     }
     __syncthreads();
 
-    // one token: the states advance, y is this lane's share of the sum over them
-    auto token = [&](int t, float delta, float dx) {
-      float bt[kStates], ct[kStates];
+    // Two tokens: the states advance, and y gets this lane's share of the sums over
+    // them.  Two tokens' arguments, additions and products are one packed
+    // instruction each.  kTail: tokens from `rows` on leave the states alone.
+    auto two = [&](auto tail, int t, float2 delta, float2 dx) {
+      constexpr bool kTail = decltype(tail)::value;
+      float2 y = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < kStates; ++i) bt[i] = bf[t * L::kWide + s0 + i];
-      if (!kEnds) {
+      for (int i = 0; i < kStates; i += 2) {
+        const float4 b4 = *reinterpret_cast<const float4*>(bf + t * L::kWide + (s0 + i) * 2);
+        float4 c4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!kEnds) c4 = *reinterpret_cast<const float4*>(cf + t * L::kWide + (s0 + i) * 2);
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) ct[i] = cf[t * L::kWide + s0 + i];
-      }
-      float y = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kStates; ++i) {
-        if (kFull || i < have) {
-          h[i] = fmaf(ex2(a2[i] * delta), h[i], dx * bt[i]);
-          if (!kEnds) y = fmaf(ct[i], h[i], y);
+        for (int j = 0; j < 2; ++j) {
+          const float2 arg = __ffma2_rn(delta, a2[i + j], make_float2(kEx2Bias, kEx2Bias));
+          const float2 add = __fmul2_rn(dx, j ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
+          float h0 = fmaf(ex2(arg.x), h[i + j], add.x);
+          if (!kFull && i + j >= have) h0 = 0.0f;
+          if (kTail && t >= rows) h0 = h[i + j];
+          float h1 = fmaf(ex2(arg.y), h0, add.y);
+          if (!kFull && i + j >= have) h1 = 0.0f;
+          if (kTail && t + 1 >= rows) h1 = h0;
+          h[i + j] = h1;
+          if (!kEnds) y = __ffma2_rn(j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), make_float2(h0, h1), y);
         }
       }
       return y;
     };
-    for (int t = 0; t < rows; t += L::kTogether) {
+    auto group = [&](auto tail, int t) {
       float y[L::kTogether];
-      if (t + L::kTogether <= rows) {
 #pragma unroll
-        for (int q = 0; q < L::kTogether; q += 4) {
-          const float4 de = *reinterpret_cast<const float4*>(delta_of + t + q);
-          const float4 dx = *reinterpret_cast<const float4*>(dx_of + t + q);
-          y[q] = token(t + q, de.x, dx.x);
-          y[q + 1] = token(t + q + 1, de.y, dx.y);
-          y[q + 2] = token(t + q + 2, de.z, dx.z);
-          y[q + 3] = token(t + q + 3, de.w, dx.w);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < L::kTogether; ++q) y[q] = t + q < rows ? token(t + q, delta_of[t + q], dx_of[t + q]) : 0.0f;
+      for (int q = 0; q < L::kTogether; q += 4) {
+        const float4 de = *reinterpret_cast<const float4*>(delta_of + t + q);
+        const float4 dx = *reinterpret_cast<const float4*>(dx_of + t + q);
+        const float2 y0 = two(tail, t + q, make_float2(de.x, de.y), make_float2(dx.x, dx.y));
+        const float2 y1 = two(tail, t + q + 2, make_float2(de.z, de.w), make_float2(dx.z, dx.w));
+        y[q] = y0.x; y[q + 1] = y0.y; y[q + 2] = y1.x; y[q + 3] = y1.y;
       }
       if constexpr (!kEnds) {
         reduce_lanes<kLanes / 2, L::kTogether>(y, lane);
 #pragma unroll
         for (int i = 0; i < L::kOwn; ++i) {
-          const int at_t = t + lane * L::kOwn + i;
-          if (at_t < rows) {
-            float v = y[i];
-            if (p.d) v = fmaf(skip, ld_f32(xr + at_t * L::kCh + cl), v);
-            if (z) v *= silu(ld_f32(zr + at_t * L::kCh + cl));
-            st_f32(out_tile + at_t * L::kCh + cl, v);
-          }
+          const int own = t + lane * L::kOwn + i;
+          float v = y[i];
+          if (p.d) v = fmaf(skip, ld_f32(xr + own * L::kPitch + cl), v);
+          if (z) v *= silu(ld_f32(zr + own * L::kPitch + cl));
+          st_f32(out_tile + own * L::kPitch + cl, v);
         }
       }
-    }
-    if constexpr (!kEnds) {
-      __syncthreads();
-      T* to = out + at * p.out_s[1];
-      if (p.out_v == 16) {
-        constexpr int E = 16 / sizeof(T);
-        const int per = w.count / E;
-        for (int i = threadIdx.x; i < rows * per; i += kThreads) {
-          const int r = i / per, q = i - r * per;
-          *reinterpret_cast<uint4*>(to + r * p.out_s[1] + q * E) = *reinterpret_cast<const uint4*>(out_tile + r * L::kCh + q * E);
-        }
-      } else {
-        for (int i = threadIdx.x; i < rows * w.count; i += kThreads) {
-          const int r = i / w.count, q = i - r * w.count;
-          to[r * p.out_s[1] + q] = out_tile[r * L::kCh + q];
-        }
-      }
-    }
+    };
+    int t = 0;
+#pragma unroll 2
+    for (; t + L::kTogether <= rows; t += L::kTogether) group(std::false_type{}, t);
+    if (t < rows) group(std::true_type{}, t);
+  }
+  if (!kEnds && begin < end) {
+    __syncthreads();
+    put(begin + (end - 1 - begin) / L::kTile * L::kTile);
   }
 
   if constexpr (kEnds) {
@@ -373,10 +392,10 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
       if constexpr (VEC) {
         float4 h = *reinterpret_cast<const float4*>(state + s);
         const float4 av = __ldg(reinterpret_cast<const float4*>(a + s));
-        h.x = fmaf(ex2(av.x * de2), h.x, dx * ld_f32(b + s));
-        h.y = fmaf(ex2(av.y * de2), h.y, dx * ld_f32(b + s + 1));
-        h.z = fmaf(ex2(av.z * de2), h.z, dx * ld_f32(b + s + 2));
-        h.w = fmaf(ex2(av.w * de2), h.w, dx * ld_f32(b + s + 3));
+        h.x = fmaf(decay(av.x, de2), h.x, dx * ld_f32(b + s));
+        h.y = fmaf(decay(av.y, de2), h.y, dx * ld_f32(b + s + 1));
+        h.z = fmaf(decay(av.z, de2), h.z, dx * ld_f32(b + s + 2));
+        h.w = fmaf(decay(av.w, de2), h.w, dx * ld_f32(b + s + 3));
         y = fmaf(ld_f32(c + s), h.x, y);
         y = fmaf(ld_f32(c + s + 1), h.y, y);
         y = fmaf(ld_f32(c + s + 2), h.z, y);
@@ -386,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (s + i >= p.states) break;
-          const float h = fmaf(ex2(__ldg(a + s + i) * de2), state[s + i], dx * ld_f32(b + s + i));
+          const float h = fmaf(decay(__ldg(a + s + i), de2), state[s + i], dx * ld_f32(b + s + i));
           y = fmaf(ld_f32(c + s + i), h, y);
           state[s + i] = h;
         }
@@ -483,6 +502,8 @@ cudaError_t step_typed(const StepArgs& p, cudaStream_t s) {
 
 }  // namespace
 
+constexpr int kChunkStep = 64;   // chunks are whole tiles
+
 // Pure in the descriptor and the device's SM count.
 ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   ScanPlan plan{};
@@ -499,13 +520,13 @@ ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   const int channels = kThreads / plan.lanes;
   const long long per_group = d.d / d.groups;
   const long long blocks = (long long)d.n * d.groups * ((per_group + channels - 1) / channels);
-  plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
+  plan.chunk = d.l > 0 ? (d.l + kChunkStep - 1) / kChunkStep * kChunkStep : kChunkStep;
   plan.chunks = 1;
   // With chunks every token is gone over twice, so three are the fewest that can pay.
-  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kTile - 1) / (2 * kTile);
+  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kChunkStep - 1) / (2 * kChunkStep);
   const long long chunks = want < most ? want : most;
   if (chunks >= 4) {
-    plan.chunk = (int)(((d.l + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
+    plan.chunk = (int)(((d.l + chunks - 1) / chunks + kChunkStep - 1) / kChunkStep * kChunkStep);
     plan.chunks = (d.l + plan.chunk - 1) / plan.chunk;
   }
   if (plan.chunks > 1) {

@@ -69,6 +69,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// ex2's results lie 0.1 to 0.4 u (u = 2^-24) below the true values on average for
+// arguments in (-1, 0), as measured over 65536 arguments a decade.  Over the many
+// tokens a slowly decaying state remembers that adds up where roundings to both
+// sides do not, so decays are taken at an argument 0.3 u / ln 2 higher.
+constexpr float kEx2Bias = 0.3f / 16777216.0f * kLog2e;
+// exp(a delta), one of the two times log2(e).
+__device__ __forceinline__ float decay(float a, float delta) { return ex2(fmaf(a, delta, kEx2Bias)); }
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
