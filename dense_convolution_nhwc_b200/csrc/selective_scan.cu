@@ -54,27 +54,42 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
 }
 
-// rows x cols elements (cols <= kCols) into shared rows kPitch elements apart, by
-// all threads; `bytes` an access, cols and every address multiples of it.
-template <typename T, int kCols, int kPitch, int N>
+// kRows x cols elements (cols <= kCols, `rows` of them there) into shared rows
+// kPitch elements apart, by all threads; `bytes` an access, cols and every address
+// multiples of it.
+template <typename T, int kRows, int kCols, int kPitch, int N>
 __device__ __forceinline__ void stage_by(T* dst, const T* src, long long stride, int rows, int cols) {
   constexpr int E = N / sizeof(T), kPer = kCols / E;
   if constexpr (E > 0 && kPer > 0) {
-    for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
-      const int r = i / kPer, q = (i % kPer) * E;
-      if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
+    constexpr int kStep = kThreads / kPer > 0 ? kThreads / kPer : 1;          // rows between a thread's accesses
+    if constexpr (kPer <= kThreads) {
+      const int r0 = threadIdx.x / kPer, q = (threadIdx.x % kPer) * E;
+      if (q < cols) {
+        src += r0 * stride + q;
+        dst += r0 * kPitch + q;
+        const long long step = kStep * stride;
+#pragma unroll
+        for (int r = 0; r < kRows; r += kStep)
+          if (r0 + r < rows && (kRows % kStep == 0 || r0 + r < kRows)) copy_async<N>(dst + r * kPitch, src + r / kStep * step);
+      }
+    } else {
+      for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
+        const int r = i / kPer, q = (i % kPer) * E;
+        if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
+      }
     }
   }
 }
-template <typename T, int kCols, int kPitch>
+template <typename T, int kRows, int kCols, int kPitch>
 __device__ __forceinline__ void stage(T* dst, const T* src, long long stride, int rows, int cols, int bytes) {
   if (bytes == 16) {
-    stage_by<T, kCols, kPitch, 16>(dst, src, stride, rows, cols);
+    stage_by<T, kRows, kCols, kPitch, 16>(dst, src, stride, rows, cols);
   } else if (bytes == 8) {
-    stage_by<T, kCols, kPitch, 8>(dst, src, stride, rows, cols);
+    stage_by<T, kRows, kCols, kPitch, 8>(dst, src, stride, rows, cols);
   } else if (bytes == 4) {
-    stage_by<T, kCols, kPitch, 4>(dst, src, stride, rows, cols);
+    stage_by<T, kRows, kCols, kPitch, 4>(dst, src, stride, rows, cols);
   } else {
+#pragma unroll 8
     for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
       const int r = i / kCols, q = i % kCols;
       if (q < cols) dst[r * kPitch + q] = src[r * stride + q];
@@ -89,6 +104,8 @@ struct Shape {
   static constexpr int kTile = kWide <= 32 ? 64 : 32;        // tokens staged together
   static constexpr int kTogether = kLanes > 8 ? kLanes : 8;  // tokens reduced together
   static constexpr int kOwn = kTogether / kLanes;            // of which each lane ends with
+  static constexpr int kSub = kStates > 4 ? 4 : 8;           // tokens whose exponentials are in flight
+  static constexpr int kMany = 32 / kTogether;               // groups in a row
   static constexpr int kRow = kTile + 8;                     // floats a channel of delta
   static constexpr int kPitch = kChannels + 16 / sizeof(T);  // elements a row of x: 16 bytes more, against bank conflicts
   // shared memory, in bytes
@@ -224,11 +241,11 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
 
   auto fetch = [&](int at, int to) {
     const int rows = min(L::kTile, end - at);
-    stage<T, L::kChannels, L::kPitch>(raw(to, 0), x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
-    stage<T, L::kChannels, L::kPitch>(raw(to, 1), dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
-    if (z) stage<T, L::kChannels, L::kPitch>(raw(to, 2), z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
-    stage<T, L::kWide, L::kWide>(raw(to, 3), b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
-    if (!kEnds) stage<T, L::kWide, L::kWide>(raw(to, 4), c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
+    stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 0), x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
+    stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 1), dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
+    if (z) stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 2), z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
+    stage<T, L::kTile, L::kWide, L::kWide>(raw(to, 3), b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
+    if (!kEnds) stage<T, L::kTile, L::kWide, L::kWide>(raw(to, 4), c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto put = [&](int at) {           // out_tile's rows, from token `at`
@@ -259,80 +276,145 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
     if (at + L::kTile < end) fetch(at + L::kTile, turn ^ 1);
 
     const T *xr = raw(turn, 0), *dr = raw(turn, 1), *zr = raw(turn, 2), *br = raw(turn, 3), *cr = raw(turn, 4);
-#pragma unroll 4
-    for (int t = lane; t < rows; t += kLanes) {
-      float delta = ld_f32(dr + t * L::kPitch + cl) + bias;
-      if (p.softplus) delta = softplus(delta);
-      delta_of[t] = delta;
-      dx_of[t] = delta * ld_f32(xr + t * L::kPitch + cl);
-      if (kEnds) sum += delta;
+    // Each pass loads all its values before it stores any: a store in between would
+    // hold back the loads after it, which the compiler cannot tell apart from it.
+    constexpr int kTurns = L::kTile / kLanes, kBatch = kTurns > 8 ? 8 : kTurns;
+#pragma unroll 1
+    for (int t0 = lane; t0 < rows; t0 += kBatch * kLanes) {
+      float de[kBatch], xv[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        de[i] = ld_f32(dr + (t0 + i * kLanes) * L::kPitch + cl) + bias;
+        xv[i] = ld_f32(xr + (t0 + i * kLanes) * L::kPitch + cl);
+      }
+      if (p.softplus) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) de[i] = softplus(de[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        delta_of[t0 + i * kLanes] = de[i];
+        dx_of[t0 + i * kLanes] = de[i] * xv[i];
+        if (kEnds && t0 + i * kLanes < rows) sum += de[i];
+      }
     }
-#pragma unroll 4
-    for (int i = threadIdx.x; i < L::kTile / 2 * L::kWide; i += kThreads) {
-      const int s = i % L::kWide, t = i / L::kWide * 2;
-      if (t < rows) {
-        const bool real = kFull || s < p.states;
-        const T *b0 = br + t * L::kWide + s, *c0 = cr + t * L::kWide + s;
-        reinterpret_cast<float2*>(bf)[i] = real ? make_float2(ld_f32(b0), ld_f32(b0 + L::kWide)) : make_float2(0.0f, 0.0f);
-        if (!kEnds)
-          reinterpret_cast<float2*>(cf)[i] = real ? make_float2(ld_f32(c0), ld_f32(c0 + L::kWide)) : make_float2(0.0f, 0.0f);
+    constexpr int kPairs = L::kTile / 2 * L::kWide, kPairTurns = (kPairs + kThreads - 1) / kThreads,
+                  kPairBatch = kPairTurns > 4 ? 4 : kPairTurns;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < kPairs && i0 / L::kWide * 2 < rows; i0 += kPairBatch * kThreads) {
+      float2 b2[kPairBatch], c2[kPairBatch];
+#pragma unroll
+      for (int k = 0; k < kPairBatch; ++k) {
+        const int i = i0 + k * kThreads, s = i % L::kWide, t = i / L::kWide * 2;
+        b2[k] = c2[k] = make_float2(0.0f, 0.0f);
+        if ((kPairs % (kPairBatch * kThreads) == 0 || i < kPairs) && (kFull || s < p.states)) {
+          const T *b0 = br + t * L::kWide + s, *c0 = cr + t * L::kWide + s;
+          b2[k] = make_float2(ld_f32(b0), ld_f32(b0 + L::kWide));
+          if (!kEnds) c2[k] = make_float2(ld_f32(c0), ld_f32(c0 + L::kWide));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPairBatch; ++k) {
+        const int i = i0 + k * kThreads;
+        if (kPairs % (kPairBatch * kThreads) == 0 || i < kPairs) {
+          reinterpret_cast<float2*>(bf)[i] = b2[k];
+          if (!kEnds) reinterpret_cast<float2*>(cf)[i] = c2[k];
+        }
       }
     }
     __syncthreads();
 
-    // Two tokens: the states advance, and y gets this lane's share of the sums over
-    // them.  Two tokens' arguments, additions and products are one packed
-    // instruction each.  kTail: tokens from `rows` on leave the states alone.
-    auto two = [&](auto tail, int t, float2 delta, float2 dx) {
+    // kSub tokens from t: the states advance, and y gets this lane's share of the sums
+    // over them.  The exponentials and additions of all tokens come first, two tokens
+    // to a packed instruction; only the h chain itself is sequential.  kTail: tokens
+    // from `rows` on leave the states alone.
+    auto sub = [&](auto tail, int t, float* y) {
       constexpr bool kTail = decltype(tail)::value;
-      float2 y = make_float2(0.0f, 0.0f);
+      constexpr int kSub = L::kSub;
+      float2 e[kSub / 2][kStates], add[kSub / 2][kStates];
 #pragma unroll
-      for (int i = 0; i < kStates; i += 2) {
-        const float4 b4 = *reinterpret_cast<const float4*>(bf + t * L::kWide + (s0 + i) * 2);
-        float4 c4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!kEnds) c4 = *reinterpret_cast<const float4*>(cf + t * L::kWide + (s0 + i) * 2);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 arg = __ffma2_rn(delta, a2[i + j], make_float2(kEx2Bias, kEx2Bias));
-          const float2 add = __fmul2_rn(dx, j ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
-          float h0 = fmaf(ex2(arg.x), h[i + j], add.x);
-          if (!kFull && i + j >= have) h0 = 0.0f;
-          if (kTail && t >= rows) h0 = h[i + j];
-          float h1 = fmaf(ex2(arg.y), h0, add.y);
-          if (!kFull && i + j >= have) h1 = 0.0f;
-          if (kTail && t + 1 >= rows) h1 = h0;
-          h[i + j] = h1;
-          if (!kEnds) y = __ffma2_rn(j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), make_float2(h0, h1), y);
-        }
-      }
-      return y;
-    };
-    auto group = [&](auto tail, int t) {
-      float y[L::kTogether];
-#pragma unroll
-      for (int q = 0; q < L::kTogether; q += 4) {
+      for (int q = 0; q < kSub; q += 4) {
         const float4 de = *reinterpret_cast<const float4*>(delta_of + t + q);
         const float4 dx = *reinterpret_cast<const float4*>(dx_of + t + q);
-        const float2 y0 = two(tail, t + q, make_float2(de.x, de.y), make_float2(dx.x, dx.y));
-        const float2 y1 = two(tail, t + q + 2, make_float2(de.z, de.w), make_float2(dx.z, dx.w));
-        y[q] = y0.x; y[q + 1] = y0.y; y[q + 2] = y1.x; y[q + 3] = y1.y;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 d2 = k ? make_float2(de.z, de.w) : make_float2(de.x, de.y);
+          const float2 x2 = k ? make_float2(dx.z, dx.w) : make_float2(dx.x, dx.y);
+#pragma unroll
+          for (int i = 0; i < kStates; i += 2) {
+            const float4 b4 = *reinterpret_cast<const float4*>(bf + (t + q + 2 * k) * L::kWide + (s0 + i) * 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 arg = __ffma2_rn(d2, a2[i + j], make_float2(kEx2Bias, kEx2Bias));
+              e[q / 2 + k][i + j] = make_float2(ex2(arg.x), ex2(arg.y));
+              add[q / 2 + k][i + j] = __fmul2_rn(x2, j ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
+            }
+          }
+        }
       }
+#pragma unroll
+      for (int q = 0; q < kSub / 2; ++q) {
+        float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kStates; i += 2) {
+          float4 c4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (!kEnds) c4 = *reinterpret_cast<const float4*>(cf + (t + 2 * q) * L::kWide + (s0 + i) * 2);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float h0 = fmaf(e[q][i + j].x, h[i + j], add[q][i + j].x);
+            if (!kFull && i + j >= have) h0 = 0.0f;
+            if (kTail && t + 2 * q >= rows) h0 = h[i + j];
+            float h1 = fmaf(e[q][i + j].y, h0, add[q][i + j].y);
+            if (!kFull && i + j >= have) h1 = 0.0f;
+            if (kTail && t + 2 * q + 1 >= rows) h1 = h0;
+            h[i + j] = h1;
+            if (!kEnds) sum2 = __ffma2_rn(j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), make_float2(h0, h1), sum2);
+          }
+        }
+        y[2 * q] = sum2.x;
+        y[2 * q + 1] = sum2.y;
+      }
+    };
+    auto group = [&](auto tail, int t, float* own) {
+      float y[L::kTogether];
+#pragma unroll
+      for (int q = 0; q < L::kTogether; q += L::kSub) sub(tail, t + q, y + q);
       if constexpr (!kEnds) {
         reduce_lanes<kLanes / 2, L::kTogether>(y, lane);
 #pragma unroll
-        for (int i = 0; i < L::kOwn; ++i) {
-          const int own = t + lane * L::kOwn + i;
-          float v = y[i];
-          if (p.d) v = fmaf(skip, ld_f32(xr + own * L::kPitch + cl), v);
-          if (z) v *= silu(ld_f32(zr + own * L::kPitch + cl));
-          st_f32(out_tile + own * L::kPitch + cl, v);
+        for (int i = 0; i < L::kOwn; ++i) own[i] = y[i];
+      }
+    };
+    // kMany groups before the outputs of any
+    auto groups = [&](auto tail, auto many, int t) {
+      constexpr int kMany = decltype(many)::value, kAll = kMany * L::kOwn;
+      float own[kAll], xv[kAll], zv[kAll];
+#pragma unroll
+      for (int g = 0; g < kMany; ++g) group(tail, t + g * L::kTogether, own + g * L::kOwn);
+      if constexpr (!kEnds) {
+#pragma unroll
+        for (int g = 0; g < kAll; ++g) {
+          const int at_t = t + g / L::kOwn * L::kTogether + lane * L::kOwn + g % L::kOwn;
+          xv[g] = ld_f32(xr + at_t * L::kPitch + cl);
+          zv[g] = z ? ld_f32(zr + at_t * L::kPitch + cl) : 0.0f;
         }
+        if (p.d) {
+#pragma unroll
+          for (int g = 0; g < kAll; ++g) own[g] = fmaf(skip, xv[g], own[g]);
+        }
+        if (z) {
+#pragma unroll
+          for (int g = 0; g < kAll; ++g) own[g] *= silu(zv[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < kAll; ++g)
+          st_f32(out_tile + (t + g / L::kOwn * L::kTogether + lane * L::kOwn + g % L::kOwn) * L::kPitch + cl, own[g]);
       }
     };
     int t = 0;
-#pragma unroll 2
-    for (; t + L::kTogether <= rows; t += L::kTogether) group(std::false_type{}, t);
-    if (t < rows) group(std::true_type{}, t);
+    for (; t + L::kMany * L::kTogether <= rows; t += L::kMany * L::kTogether)
+      groups(std::false_type{}, std::integral_constant<int, L::kMany>{}, t);
+    for (; t < rows; t += L::kTogether) groups(std::true_type{}, std::integral_constant<int, 1>{}, t);
   }
   if (!kEnds && begin < end) {
     __syncthreads();
