@@ -54,48 +54,62 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
 }
 
-// kRows x cols elements (cols <= kCols, `rows` of them there) into shared rows
-// kPitch elements apart, by all threads; `bytes` an access, cols and every address
-// multiples of it.
-template <typename T, int kRows, int kCols, int kPitch, int N>
-__device__ __forceinline__ void stage_by(T* dst, const T* src, long long stride, int rows, int cols) {
-  constexpr int E = N / sizeof(T), kPer = kCols / E;
-  if constexpr (E > 0 && kPer > 0) {
-    constexpr int kStep = kThreads / kPer > 0 ? kThreads / kPer : 1;          // rows between a thread's accesses
-    if constexpr (kPer <= kThreads) {
-      const int r0 = threadIdx.x / kPer, q = (threadIdx.x % kPer) * E;
-      if (q < cols) {
-        src += r0 * stride + q;
-        dst += r0 * kPitch + q;
-        const long long step = kStep * stride;
-#pragma unroll
-        for (int r = 0; r < kRows; r += kStep)
-          if (r0 + r < rows && (kRows % kStep == 0 || r0 + r < kRows)) copy_async<N>(dst + r * kPitch, src + r / kStep * step);
-      }
-    } else {
-      for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
-        const int r = i / kPer, q = (i % kPer) * E;
-        if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
-      }
-    }
-  }
-}
+// Copies tiles of kRows x cols elements (cols <= kCols) of a tensor's consecutive
+// rows into shared rows kPitch elements apart, by all threads.  `bytes`: an access
+// (16, 8, 4, or 0 for single elements), cols and every address multiples of it.
+// The 16-byte form keeps each thread's address from tile to tile: worked out anew,
+// the five tensors' addresses took as long as a third of the recursion itself.
 template <typename T, int kRows, int kCols, int kPitch>
-__device__ __forceinline__ void stage(T* dst, const T* src, long long stride, int rows, int cols, int bytes) {
-  if (bytes == 16) {
-    stage_by<T, kRows, kCols, kPitch, 16>(dst, src, stride, rows, cols);
-  } else if (bytes == 8) {
-    stage_by<T, kRows, kCols, kPitch, 8>(dst, src, stride, rows, cols);
-  } else if (bytes == 4) {
-    stage_by<T, kRows, kCols, kPitch, 4>(dst, src, stride, rows, cols);
-  } else {
-#pragma unroll 8
-    for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
-      const int r = i / kCols, q = i % kCols;
-      if (q < cols) dst[r * kPitch + q] = src[r * stride + q];
+struct Stager {
+  static constexpr int E = 16 / sizeof(T), kPer = kCols / E > 0 ? kCols / E : 1;
+  static constexpr int kStep = kThreads / kPer > 0 ? kThreads / kPer : 1;     // rows between a thread's accesses
+  static constexpr bool kFits = kCols % E == 0 && kPer <= kThreads && kRows % kStep == 0;
+  const T* src;
+  long long stride;
+  int cols, bytes, r0, to;
+  __device__ __forceinline__ void init(const T* base, long long row_stride, int width, int access) {
+    src = base;
+    stride = row_stride;
+    cols = width;
+    bytes = access;
+    r0 = threadIdx.x / kPer;
+    const int q = (threadIdx.x % kPer) * E;
+    to = r0 * kPitch + q;
+    if (kFits && bytes == 16) {
+      src += r0 * stride + q;
+      if (q >= cols) r0 = kRows;        // past the edge: never a row
     }
   }
-}
+  template <int N>
+  __device__ __forceinline__ void by(T* dst, int rows) {
+    constexpr int kE = N / sizeof(T) > 0 ? N / sizeof(T) : 1, kAcross = kCols / kE > 0 ? kCols / kE : 1;
+    for (int i = threadIdx.x; i < rows * kAcross; i += kThreads) {
+      const int r = i / kAcross, q = (i % kAcross) * kE;
+      if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
+    }
+  }
+  // The next `rows` rows.
+  __device__ __forceinline__ void next(T* dst, int rows) {
+    if (kFits && bytes == 16) {
+#pragma unroll
+      for (int r = 0; r < kRows; r += kStep)
+        if (r0 + r < rows) copy_async<16>(dst + to + r * kPitch, src + r * stride);
+    } else if (bytes == 16) {
+      by<16>(dst, rows);
+    } else if (bytes == 8) {
+      by<8>(dst, rows);
+    } else if (bytes == 4) {
+      by<4>(dst, rows);
+    } else {
+#pragma unroll 8
+      for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
+        const int r = i / kCols, q = i % kCols;
+        if (q < cols) dst[r * kPitch + q] = src[r * stride + q];
+      }
+    }
+    src += kRows * stride;
+  }
+};
 
 template <typename T, int kStates, int kLanes>
 struct Shape {
@@ -116,7 +130,7 @@ struct Shape {
   static constexpr int kDelta = kOut + kRawX;
   static constexpr int kB = kDelta + 2 * kChannels * kRow * 4;
   static constexpr int kBytes = kB + 2 * kTile * kWide * 4;
-  static_assert(kTile % kTogether == 0 && kStates % 2 == 0, "");
+  static_assert(kTile % kTogether == 0 && (kStates == 1 || kStates % 2 == 0), "");
 };
 
 // Sequence, channel tile and tokens of a block.
@@ -149,6 +163,21 @@ template <typename T>
 __device__ __forceinline__ const T* rows_of(const ScanArgs& p, const void* base, const long long (&s)[2], const Where& w,
                                             int col) {
   return static_cast<const T*>(base) + (p.offsets ? 0 : w.seq * s[0]) + w.lo * s[1] + col;
+}
+
+// The values of two tokens for each of kStates neighbouring states.
+template <int kStates>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[kStates]) {
+  if constexpr (kStates == 1) {
+    v[0] = *reinterpret_cast<const float2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kStates; i += 2) {
+      const float4 two = *reinterpret_cast<const float4*>(p + 2 * i);
+      v[i] = make_float2(two.x, two.y);
+      v[i + 1] = make_float2(two.z, two.w);
+    }
+  }
 }
 
 // The sums over a channel's lanes of kCount tokens' y: at each step a lane passes on
@@ -239,13 +268,20 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
   float* bf = reinterpret_cast<float*>(smem + L::kB);
   float* cf = bf + L::kTile * L::kWide;
 
+  Stager<T, L::kTile, L::kChannels, L::kPitch> sx, sdt, sz;
+  Stager<T, L::kTile, L::kWide, L::kWide> sb, sc;
+  sx.init(x + begin * p.x_s[1], p.x_s[1], w.count, p.x_v);
+  sdt.init(dt + begin * p.dt_s[1], p.dt_s[1], w.count, p.dt_v);
+  sb.init(b + begin * p.b_s[1], p.b_s[1], p.states, p.b_v);
+  if (z) sz.init(z + begin * p.z_s[1], p.z_s[1], w.count, p.z_v);
+  if (!kEnds) sc.init(c + begin * p.c_s[1], p.c_s[1], p.states, p.c_v);
   auto fetch = [&](int at, int to) {
     const int rows = min(L::kTile, end - at);
-    stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 0), x + at * p.x_s[1], p.x_s[1], rows, w.count, p.x_v);
-    stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 1), dt + at * p.dt_s[1], p.dt_s[1], rows, w.count, p.dt_v);
-    if (z) stage<T, L::kTile, L::kChannels, L::kPitch>(raw(to, 2), z + at * p.z_s[1], p.z_s[1], rows, w.count, p.z_v);
-    stage<T, L::kTile, L::kWide, L::kWide>(raw(to, 3), b + at * p.b_s[1], p.b_s[1], rows, p.states, p.b_v);
-    if (!kEnds) stage<T, L::kTile, L::kWide, L::kWide>(raw(to, 4), c + at * p.c_s[1], p.c_s[1], rows, p.states, p.c_v);
+    sx.next(raw(to, 0), rows);
+    sdt.next(raw(to, 1), rows);
+    if (z) sz.next(raw(to, 2), rows);
+    sb.next(raw(to, 3), rows);
+    if (!kEnds) sc.next(raw(to, 4), rows);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto put = [&](int at) {           // out_tile's rows, from token `at`
@@ -341,35 +377,30 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
           const float2 d2 = k ? make_float2(de.z, de.w) : make_float2(de.x, de.y);
           const float2 x2 = k ? make_float2(dx.z, dx.w) : make_float2(dx.x, dx.y);
 #pragma unroll
-          for (int i = 0; i < kStates; i += 2) {
-            const float4 b4 = *reinterpret_cast<const float4*>(bf + (t + q + 2 * k) * L::kWide + (s0 + i) * 2);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 arg = __ffma2_rn(d2, a2[i + j], make_float2(kEx2Bias, kEx2Bias));
-              e[q / 2 + k][i + j] = make_float2(ex2(arg.x), ex2(arg.y));
-              add[q / 2 + k][i + j] = __fmul2_rn(x2, j ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
-            }
+          for (int i = 0; i < kStates; ++i) {
+            const float2 arg = __ffma2_rn(d2, a2[i], make_float2(kEx2Bias, kEx2Bias));
+            e[q / 2 + k][i] = make_float2(ex2(arg.x), ex2(arg.y));
           }
+          load_pairs<kStates>(bf + (t + q + 2 * k) * L::kWide + s0 * 2, add[q / 2 + k]);
+#pragma unroll
+          for (int i = 0; i < kStates; ++i) add[q / 2 + k][i] = __fmul2_rn(x2, add[q / 2 + k][i]);
         }
       }
 #pragma unroll
       for (int q = 0; q < kSub / 2; ++q) {
         float2 sum2 = make_float2(0.0f, 0.0f);
+        float2 ct[kStates];
+        if (!kEnds) load_pairs<kStates>(cf + (t + 2 * q) * L::kWide + s0 * 2, ct);
 #pragma unroll
-        for (int i = 0; i < kStates; i += 2) {
-          float4 c4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (!kEnds) c4 = *reinterpret_cast<const float4*>(cf + (t + 2 * q) * L::kWide + (s0 + i) * 2);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float h0 = fmaf(e[q][i + j].x, h[i + j], add[q][i + j].x);
-            if (!kFull && i + j >= have) h0 = 0.0f;
-            if (kTail && t + 2 * q >= rows) h0 = h[i + j];
-            float h1 = fmaf(e[q][i + j].y, h0, add[q][i + j].y);
-            if (!kFull && i + j >= have) h1 = 0.0f;
-            if (kTail && t + 2 * q + 1 >= rows) h1 = h0;
-            h[i + j] = h1;
-            if (!kEnds) sum2 = __ffma2_rn(j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), make_float2(h0, h1), sum2);
-          }
+        for (int i = 0; i < kStates; ++i) {
+          float h0 = fmaf(e[q][i].x, h[i], add[q][i].x);
+          if (!kFull && i >= have) h0 = 0.0f;
+          if (kTail && t + 2 * q >= rows) h0 = h[i];
+          float h1 = fmaf(e[q][i].y, h0, add[q][i].y);
+          if (!kFull && i >= have) h1 = 0.0f;
+          if (kTail && t + 2 * q + 1 >= rows) h1 = h0;
+          h[i] = h1;
+          if (!kEnds) sum2 = __ffma2_rn(ct[i], make_float2(h0, h1), sum2);
         }
         y[2 * q] = sum2.x;
         y[2 * q + 1] = sum2.y;
