@@ -2,7 +2,8 @@
 
 The library itself is the C-ABI shared object built from ``csrc/`` (declared in
 ``include/b200conv.h``); ``binding`` marshals arguments into it with ctypes and
-nothing else.  The binding is loaded on first use of one of its names, and
+nothing else, and ``sequence`` holds the torch conveniences of the sequence
+operators.  The binding is loaded on first use of one of its names, and
 loading fails loudly if the shared object has not been built: there is no CPU
 fallback.
 """
@@ -23,12 +24,16 @@ _BINDING_NAMES = frozenset({
     "CausalConvDesc", "ScanDesc", "ScanTensors", "ScanPlan", "ACTIVATION",
     # torch conveniences
     "conv1d", "conv2d", "conv3d", "plan2d", "plan3d",
-    "conv1d_causal", "conv1d_causal_step", "selective_scan", "selective_scan_step",
 })
+_SEQUENCE_NAMES = frozenset({"conv1d_causal", "conv1d_causal_step", "selective_scan", "selective_scan_step"})
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)
+    if name in _SEQUENCE_NAMES:
+        from . import sequence
+        # found here from now on: a decoding step calls these by the thousand
+        return globals().setdefault(name, getattr(sequence, name))
     raise AttributeError(f"module 'dense_convolution_nhwc_b200' has no attribute {name!r}")

@@ -80,18 +80,16 @@ class ConvPlan(ctypes.Structure):
 
 
 class CausalConvDesc(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int), ("l", ctypes.c_int), ("c", ctypes.c_int), ("k", ctypes.c_int),
-                ("activation", ctypes.c_int), ("carry", ctypes.c_int), ("state_slots", ctypes.c_int),
-                ("x_stride", ctypes.c_longlong * 2), ("out_stride", ctypes.c_longlong * 2)]
+    """conv1d_causal_desc_t, its stride arrays' elements as fields of their own."""
+    _fields_ = [(name, ctypes.c_int) for name in ("n", "l", "c", "k", "activation", "carry", "state_slots")] + \
+               [(f"{name}_stride_{of}", ctypes.c_longlong) for name in ("x", "out") for of in ("batch", "token")]
 
 
 class ScanDesc(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int), ("l", ctypes.c_int), ("d", ctypes.c_int), ("s", ctypes.c_int),
-                ("groups", ctypes.c_int), ("softplus", ctypes.c_int), ("carry", ctypes.c_int),
-                ("state_slots", ctypes.c_int), ("x_stride", ctypes.c_longlong * 2),
-                ("dt_stride", ctypes.c_longlong * 2), ("z_stride", ctypes.c_longlong * 2),
-                ("b_stride", ctypes.c_longlong * 2), ("c_stride", ctypes.c_longlong * 2),
-                ("out_stride", ctypes.c_longlong * 2)]
+    """selective_scan_desc_t, its stride arrays' elements as fields of their own."""
+    _fields_ = [(name, ctypes.c_int) for name in ("n", "l", "d", "s", "groups", "softplus", "carry", "state_slots")] + \
+               [(f"{name}_stride_{of}", ctypes.c_longlong) for name in ("x", "dt", "z", "b", "c", "out")
+                for of in ("batch", "token")]
 
 
 class ScanTensors(ctypes.Structure):
@@ -550,208 +548,4 @@ def conv3d(x, w, stride=1, padding=0, dilation=1, options: Optional[ConvOptions]
         st = conv3d_forward(x.data_ptr(), w.data_ptr(), out.data_ptr(), desc, dt, options, ws_ptr, ws_n, stream)
         if st != 0:
             raise ConvError(st, "conv3d_forward")
-    return out
-
-
-# ---------------------------------------------------------------------------
-# Sequence operators: the short causal conv1d and the selective scan
-# ---------------------------------------------------------------------------
-
-def _operand(t, name, shape, dtype, device, dense=False):
-    """A tensor of the call: its pointer, after the checks that the C ABI cannot
-    make.  dense: contiguous; else the last dimension is.  Raises before any launch."""
-    if t is None:
-        return 0
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, x on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dense:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr()
-
-
-def _strides(t, packed):
-    """{batch, token} strides; a packed buffer and a step's rows have one of them."""
-    s = t.stride()
-    return (0, s[0]) if packed else (s[0], s[1])
-
-
-def _sequences(x, offsets, carry, state, slots):
-    """(packed, sequences, tokens) of a prompt call."""
-    torch = _torch()
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError("x must be a CUDA tensor (the library has no CPU path)")
-    packed = offsets is not None
-    if x.dim() != (2 if packed else 3):
-        raise ValueError("x must be [T, C] with offsets, [N, L, C] without")
-    if packed and (not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1):
-        raise ValueError("offsets must be a tensor of n + 1 values")
-    if state is None and (carry or slots is not None):
-        raise ValueError("carry and slots need a state")
-    return packed, offsets.shape[0] - 1 if packed else x.shape[0], x.shape[0] if packed else x.shape[1]
-
-
-def _cache(state, slots, n, tail, dtype, device):
-    """(state pointer, slots pointer, slots in the cache) for n sequences."""
-    if state is None:
-        return 0, 0, 0
-    if not isinstance(state, _torch().Tensor) or state.dim() != 3:
-        raise ValueError(f"state must be a tensor of shape (slots, {tail[0]}, {tail[1]})")
-    ptr = _operand(state, "state", (state.shape[0], *tail), dtype, device, dense=True)
-    if slots is None and state.shape[0] < n:
-        raise ValueError(f"state has {state.shape[0]} slots for {n} sequences")
-    if slots is not None and state.shape[0] < 1:
-        raise ValueError("state has no slots")
-    return ptr, _operand(slots, "slots", (n,), _torch().int32, device, dense=True), state.shape[0]
-
-
-def _enqueue(device, call, where):
-    """call(stream) on the device of the tensors and torch's current stream there."""
-    cuda = _torch().cuda
-    if device.index == cuda.current_device():
-        st = call(cuda.current_stream(device).cuda_stream)
-    else:
-        with cuda.device(device):
-            st = call(cuda.current_stream(device).cuda_stream)
-    if st != 0:
-        raise ConvError(st, where)
-
-
-def _activation(name):
-    if name not in ACTIVATION:
-        raise ValueError(f"activation {name!r}: expected None or 'silu'")
-    return ACTIVATION[name]
-
-
-def conv1d_causal(x, w, bias=None, activation=None, offsets=None, state=None, slots=None, carry=False, out=None):
-    """Short depthwise causal conv1d over prompts, w [C, K] with 2 <= K <= 8, the last
-    tap on the token itself: x [N, L, C], or packed [T, C] with int32 offsets [n + 1]
-    (rows outside every sequence are left as they are).  The K-1 tokens before a
-    sequence are zero, or with carry its slot of state [slots, K-1, C]; the last K-1
-    tokens are left in state where one is given.  x may be a slice of wider rows."""
-    packed, n, l = _sequences(x, offsets, carry, state, slots)
-    dt, device = _dtype_code(x.dtype), x.device
-    c = x.shape[-1]
-    xp = _operand(x, "x", x.shape, x.dtype, device)
-    if not isinstance(w, _torch().Tensor) or w.dim() != 2:
-        raise ValueError("w must be a tensor of shape [C, K]")
-    k = w.shape[1]
-    wp = _operand(w, "w", (c, k), x.dtype, device, dense=True)
-    bp = _operand(bias, "bias", (c,), x.dtype, device, dense=True)
-    op = _operand(offsets, "offsets", (n + 1,), _torch().int32, device, dense=True)
-    sp, ip, slots_n = _cache(state, slots, n, (k - 1, c), x.dtype, device)
-    if out is None:
-        out = _torch().empty(x.shape, dtype=x.dtype, device=device)
-    yp = _operand(out, "out", x.shape, x.dtype, device)
-    desc = CausalConvDesc(n, l, c, k, _activation(activation), 1 if carry else 0, slots_n, _strides(x, packed),
-                          _strides(out, packed))
-    _enqueue(device, lambda s: conv1d_causal_forward(xp, wp, bp, op, sp, ip, yp, desc, dt, s), "conv1d_causal_forward")
-    return out
-
-
-def conv1d_causal_step(x, w, state, bias=None, activation=None, slots=None, out=None):
-    """conv1d_causal for one new token of each of N sequences: x [N, C], the window of
-    sequence i in slot i, or slots[i], of state [slots, K-1, C], shifted in place.  A
-    sequence whose slot is outside the cache (-1) is left out, its row of out too."""
-    if not isinstance(x, _torch().Tensor) or not x.is_cuda:
-        raise TypeError("x must be a CUDA tensor (the library has no CPU path)")
-    if x.dim() != 2 or not isinstance(w, _torch().Tensor) or w.dim() != 2 or state is None:
-        raise ValueError("x must be [N, C], w [C, K], state [slots, K-1, C]")
-    dt, device = _dtype_code(x.dtype), x.device
-    (n, c), k = x.shape, w.shape[1]
-    xp = _operand(x, "x", x.shape, x.dtype, device)
-    wp = _operand(w, "w", (c, k), x.dtype, device, dense=True)
-    bp = _operand(bias, "bias", (c,), x.dtype, device, dense=True)
-    sp, ip, slots_n = _cache(state, slots, n, (k - 1, c), x.dtype, device)
-    if out is None:
-        out = _torch().empty((n, c), dtype=x.dtype, device=device)
-    yp = _operand(out, "out", (n, c), x.dtype, device)
-    desc = CausalConvDesc(n, 1, c, k, _activation(activation), 1, slots_n, (x.stride(0), 0), (out.stride(0), 0))
-    _enqueue(device, lambda s: conv1d_causal_step_forward(xp, wp, bp, sp, ip, yp, desc, dt, s),
-             "conv1d_causal_step_forward")
-    return out
-
-
-def _scan_operands(x, dt, a, b, c, d, z, dt_bias, lead):
-    """(pointers of x, dt, b, c, z, a, d, dt_bias; groups; states) of a scan or a step."""
-    f32, device, io = _torch().float32, x.device, x.dtype
-    dim = x.shape[-1]
-    if not isinstance(b, _torch().Tensor) or b.dim() != len(lead) + 2:
-        raise ValueError("b must be a tensor of shape [..., G, S]")
-    g, s = b.shape[-2:]
-    if g < 1 or dim % g:
-        raise ValueError(f"{g} groups do not divide {dim} channels")
-    for t, name in ((b, "b"), (c, "c")):
-        if isinstance(t, _torch().Tensor) and t.dim() == b.dim() and g > 1 and t.stride(-2) != s:
-            raise ValueError(f"the last two dimensions of {name} must be contiguous")
-    return (_operand(x, "x", x.shape, io, device), _operand(dt, "dt", x.shape, io, device),
-            _operand(b, "b", (*lead, g, s), io, device), _operand(c, "c", (*lead, g, s), io, device),
-            _operand(z, "z", x.shape, io, device), _operand(a, "a", (dim, s), f32, device, dense=True),
-            _operand(d, "d", (dim,), f32, device, dense=True),
-            _operand(dt_bias, "dt_bias", (dim,), f32, device, dense=True)), g, s
-
-
-def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=False, offsets=None, state=None, slots=None,
-                   carry=False, out=None, workspace=None):
-    """The selective state space recurrence over prompts, per channel and state:
-    h_t = exp(delta_t a) h_{t-1} + delta_t b_t x_t, out_t = (c_t . h_t + d x_t) silu(z_t),
-    delta_t = dt_t + dt_bias, through log(1 + exp(.)) with softplus.
-
-    x, dt, z [N, L, D], b, c [N, L, G, S], or packed [T, D], [T, G, S] with int32 offsets
-    [n + 1] (rows outside every sequence are left as they are); a [D, S], d, dt_bias [D]
-    in fp32.  h starts from zero, or with carry from state [slots, D, S] (fp32), and is
-    left there where one is given.  x, dt, z, b, c may be slices of wider rows."""
-    torch = _torch()
-    packed, n, l = _sequences(x, offsets, carry, state, slots)
-    code, device = _dtype_code(x.dtype), x.device
-    ptrs, g, s = _scan_operands(x, dt, a, b, c, d, z, dt_bias, x.shape[:-1])
-    dim = x.shape[-1]
-    op = _operand(offsets, "offsets", (n + 1,), torch.int32, device, dense=True)
-    sp, ip, slots_n = _cache(state, slots, n, (dim, s), torch.float32, device)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-    yp = _operand(out, "out", x.shape, x.dtype, device)
-    desc = ScanDesc(n, l, dim, s, g, 1 if softplus else 0, 1 if carry else 0, slots_n, _strides(x, packed),
-                    _strides(dt, packed), (0, 0) if z is None else _strides(z, packed), _strides(b, packed),
-                    _strides(c, packed), _strides(out, packed))
-    need = selective_scan_workspace_size(desc, code, device.index)
-    if workspace is not None:
-        _check_workspace(workspace, need, x)
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    tensors = ScanTensors(*ptrs, op, ip, sp, yp)
-    ws, ws_n = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _enqueue(device, lambda st: selective_scan_forward(tensors, desc, code, ws, ws_n, st), "selective_scan_forward")
-    return out
-
-
-def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, softplus=False, slots=None, out=None):
-    """selective_scan for one new token of each of N sequences: x, dt, z [N, D], b, c
-    [N, G, S], the state of sequence i in slot i, or slots[i], of state [slots, D, S]
-    (fp32), advanced in place.  A sequence whose slot is outside the cache (-1) is left
-    out, its row of out too."""
-    torch = _torch()
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError("x must be a CUDA tensor (the library has no CPU path)")
-    if x.dim() != 2 or state is None:
-        raise ValueError("x must be [N, D], state [slots, D, S]")
-    code, device = _dtype_code(x.dtype), x.device
-    ptrs, g, s = _scan_operands(x, dt, a, b, c, d, z, dt_bias, x.shape[:-1])
-    n, dim = x.shape
-    sp, ip, slots_n = _cache(state, slots, n, (dim, s), torch.float32, device)
-    if out is None:
-        out = torch.empty((n, dim), dtype=x.dtype, device=device)
-    yp = _operand(out, "out", (n, dim), x.dtype, device)
-    desc = ScanDesc(n, 1, dim, s, g, 1 if softplus else 0, 1, slots_n, (x.stride(0), 0), (dt.stride(0), 0),
-                    (0, 0) if z is None else (z.stride(0), 0), (b.stride(0), 0), (c.stride(0), 0), (out.stride(0), 0))
-    tensors = ScanTensors(*ptrs, 0, ip, sp, yp)
-    _enqueue(device, lambda st: selective_scan_step_forward(tensors, desc, code, st), "selective_scan_step_forward")
     return out

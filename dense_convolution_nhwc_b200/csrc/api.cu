@@ -75,6 +75,21 @@ conv_status_t device_state(int dev, DeviceState** out) {
   return CONV_OK;
 }
 
+// The SM count alone, without the error word's lookup (the sequence operators have no waits to report).
+conv_status_t device_sm_count(int dev, int* sms) {
+  if (dev >= 0 && dev < kMaxDevices) {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (g_dev[dev].ready) {
+      *sms = g_dev[dev].props.sm_count;
+      return CONV_OK;
+    }
+  }
+  DeviceState* d = nullptr;
+  conv_status_t st = device_state(dev, &d);
+  if (st == CONV_OK) *sms = d->props.sm_count;
+  return st;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 long long out_extent(long long in, int k, int s, int p, int d) {
@@ -1305,8 +1320,9 @@ conv_status_t selective_scan_plan(const selective_scan_desc_t* desc, conv_dtype_
 }
 
 size_t selective_scan_workspace_size(const selective_scan_desc_t* desc, conv_dtype_t dtype, int device) {
-  selective_scan_plan_t p;
-  return selective_scan_plan(desc, dtype, device, &p) == CONV_OK ? p.workspace_bytes : 0;
+  int sms = 0;
+  if (check_scan(desc, dtype) != CONV_OK || device_sm_count(device, &sms) != CONV_OK) return 0;
+  return plan_scan(*desc, sms).workspace_bytes;
 }
 
 conv_status_t selective_scan_forward(const selective_scan_tensors_t* tensors, const selective_scan_desc_t* desc,
@@ -1319,10 +1335,10 @@ conv_status_t selective_scan_forward(const selective_scan_tensors_t* tensors, co
   if (st != CONV_OK) return st;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return CONV_ERR_CUDA;
-  DeviceState* d = nullptr;
-  st = device_state(dev, &d);
+  int sms = 0;
+  st = device_sm_count(dev, &sms);
   if (st != CONV_OK) return st;
-  const ScanPlan plan = plan_scan(*desc, d->props.sm_count);
+  const ScanPlan plan = plan_scan(*desc, sms);
   if (workspace_bytes < plan.workspace_bytes || (plan.workspace_bytes > 0 && !workspace)) return CONV_ERR_WORKSPACE;
   if (plan.workspace_bytes > 0 && !aligned256(workspace)) return CONV_ERR_ALIGNMENT;
   if (log_enabled())

@@ -8,8 +8,15 @@
 //
 // Bound by memory: every input is read once and every output written once, with
 // K FMAs (and an exp and a reciprocal) a value.  A thread owns 16 bytes of
-// channels and walks kTokens rows with the last K-1 rows in registers, so x is
-// read once but for the K-1 rows before each walk (from L2).
+// channels and walks up to 64 rows with the last K-1 rows in registers, so x is
+// read once but for the K-1 rows before each walk (from L2).  Rows come through a
+// ring of eight in shared memory that each thread fills for itself with cp.async:
+// the bytes in flight then cost no registers, of which the taps and the window
+// (2K - 1 values a channel) already take most.  4 x 4096 rows of 4096 bf16 channels,
+// K = 4, silu: 51 us = 5.3 TB/s, 81 % of the copy rate; with the rows in flight held
+// in registers (8 at a time, twice) 64 us, without any in flight while the others
+// are worked on 91 us.  Two or four rows worked on together, eight channel bytes a
+// thread, or registers capped for more blocks an SM: 52 to 120 us.
 #include <cuda_runtime.h>
 
 #include "sequence.cuh"
@@ -18,8 +25,9 @@ namespace b200conv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTokens = 32;   // rows of one thread's walk
-constexpr int kBatch = 8;     // rows loaded together
+constexpr int kBatch = 1;      // rows worked on together
+constexpr int kAhead = 8;      // rows on their way
+constexpr int kBytes = 16;     // of channels a thread
 
 struct ConvArgs {
   const void *x, *w, *bias;
@@ -28,8 +36,17 @@ struct ConvArgs {
   int n, l, c, state_slots, silu, carry;
   long long x_sn, x_st, o_sn, o_st;
   int groups;       // channel vectors a row
+  int tokens;       // rows of one thread's walk
   int tiles;        // walks a sequence (dense) or a call (packed)
 };
+
+// Threads are laid out over channel vectors (x) and walks or sequences (y), so that
+// none has to divide: a row of blocks along x covers the channels.
+__device__ __forceinline__ bool my_place(int groups, int* group, long long* item) {
+  *group = blockIdx.x * blockDim.x + threadIdx.x;
+  *item = ((long long)blockIdx.z * gridDim.y + blockIdx.y) * blockDim.y + threadIdx.y;
+  return *group < groups;
+}
 
 // The taps of V channels: [V][K] in memory, [K][V] in registers.
 template <typename T, int K, int V, bool VEC>
@@ -41,6 +58,22 @@ __device__ __forceinline__ void load_taps(const T* p, float (&w)[K][V]) {
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k][v] = flat[(v * K + k) / V][(v * K + k) % V];
+}
+
+// acc += w * x, two channels to a packed instruction.
+template <int V>
+__device__ __forceinline__ void multiply_add(const float (&w)[V], const float (&x)[V], float (&acc)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      const float2 r = __ffma2_rn(make_float2(w[v], w[v + 1]), make_float2(x[v], x[v + 1]), make_float2(acc[v], acc[v + 1]));
+      acc[v] = r.x;
+      acc[v + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(w[v], x[v], acc[v]);
+  }
 }
 
 template <typename T, int K, int V, bool VEC>
@@ -74,37 +107,96 @@ struct Walk {
     }
   }
 
+  // The next output from the window and the row after it, which the window takes up.
+  __device__ __forceinline__ void step(float (&win)[K - 1][V], const float (&now)[V], float (&acc)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = b[v];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) multiply_add<V>(w[k], win[k], acc);
+    multiply_add<V>(w[K - 1], now, acc);
+    if (p.silu) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = silu(acc[v]);
+    }
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[k][v] = k < K - 2 ? win[k < K - 2 ? k + 1 : k][v] : now[v];
+  }
+
   // Positions [from, to) of the sequence whose rows start at x and out.
   __device__ __forceinline__ void run(const T* x, T* out, int from, int to, int slot) const {
     if (from >= to) return;
     float win[K - 1][V];
+    const T* ahead = x + from * p.x_st;
+    T* here = out + from * p.o_st;
+    if constexpr (VEC) {
+      // kAhead rows of this thread's own 16 bytes are on their way into shared memory
+      // while kBatch rows are worked on.  Only the thread itself reads them, so its
+      // own copies are all it waits for.
+      extern __shared__ uint4 ring[];
+      uint4* mine = ring + threadIdx.y * blockDim.x + threadIdx.x;
+      const int step_of = blockDim.x * blockDim.y;
+      auto fetch = [&](int row_in_ring, int count) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
-    for (int at = from; at < to; at += kBatch) {
-      float in[kBatch][V];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (at + u < to) load_f32<T, V, VEC>(x + (at + u) * p.x_st, in[u]);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (at + u >= to) break;
-        float acc[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          acc[v] = b[v];
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const int j = u + k - (K - 1);      // row at + j
-            acc[v] = fmaf(w[k][v], j < 0 ? win[j + K - 1][v] : in[j < 0 ? 0 : j][v], acc[v]);
-          }
-          if (p.silu) acc[v] = silu(acc[v]);
+        for (int u = 0; u < kBatch; ++u) {
+          if (u < count) copy_async<16>(mine + (row_in_ring + u) * step_of, ahead);
+          ahead += p.x_st;
         }
-        store_f32<T, V, VEC>(out + (at + u) * p.o_st, acc);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int f = 0; f < kAhead / kBatch; ++f) fetch(f * kBatch, to - from - f * kBatch);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
+      for (int at = from, slot_in_ring = 0; at < to; at += kBatch) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / kBatch - 1) : "memory");
+        float now[kBatch][V];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          load_f32<T, V, true>(reinterpret_cast<const T*>(mine + (slot_in_ring + u) * step_of), now[u]);
+        fetch(slot_in_ring, to - at - kAhead);
+        slot_in_ring = slot_in_ring + kBatch == kAhead ? 0 : slot_in_ring + kBatch;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          float acc[V];
+          step(win, now[u], acc);
+          if (at + u < to) store_f32<T, V, true>(here, acc);
+          here += p.o_st;
+        }
       }
+      // a later walk of this thread reuses the ring: nothing may be on its way into it
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
+      for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
+      T in[kBatch][V], next[kBatch][V];
+      auto fetch = [&](T(&to_regs)[kBatch][V], int count) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) win[j][v] = in[kBatch - (K - 1) + j][v];
+        for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (u < count) to_regs[u][v] = ahead[v];
+          ahead += p.x_st;
+        }
+      };
+      fetch(in, to - from);
+      for (int at = from; at < to; at += kBatch) {
+        fetch(next, to - at - kBatch);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          float acc[V], now[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) now[v] = Store<T>::to_f32(in[u][v]);
+          step(win, now, acc);
+          if (at + u < to) store_f32<T, V, false>(here, acc);
+          here += p.o_st;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int v = 0; v < V; ++v) in[u][v] = next[u][v];
+      }
     }
   }
 
@@ -122,35 +214,43 @@ struct Walk {
 
 template <typename T, int K, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) causal_conv_kernel(const ConvArgs p) {
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long walk_id = id / p.groups;
-  const int ch = (int)(id - walk_id * p.groups) * V;
+  int place;
+  long long walk_id;
+  if (!my_place(p.groups, &place, &walk_id)) return;
+  const int ch = place * V;
   const T* x = static_cast<const T*>(p.x) + ch;
   T* out = static_cast<T*>(p.out) + ch;
   if (!p.offsets) {
     if (walk_id >= (long long)p.n * p.tiles) return;
-    const int seq = (int)(walk_id / p.tiles);
-    const int from = (int)(walk_id - (long long)seq * p.tiles) * kTokens;
+    const int seq = (int)(walk_id < 0x7fffffff ? (unsigned)walk_id / (unsigned)p.tiles : walk_id / p.tiles);
+    const int from = (int)(walk_id - (long long)seq * p.tiles) * p.tokens;
     const int slot = slot_of(p.slots, seq, p.state_slots);
     if (slot < 0) return;
     const Walk<T, K, V, VEC> walk(p, ch);
     x += seq * p.x_sn;
-    walk.run(x, out + seq * p.o_sn, from, min(from + kTokens, p.l), slot);
+    walk.run(x, out + seq * p.o_sn, from, min(from + p.tokens, p.l), slot);
     if (p.state && from == 0) walk.keep(x, p.l, slot);
     return;
   }
   if (walk_id >= p.tiles) return;
-  const int first = (int)walk_id * kTokens;
+  const int first = (int)walk_id * p.tokens;
   const bool last_walk = walk_id == p.tiles - 1;
-  const int end = last_walk ? p.l : first + kTokens;
+  const int end = last_walk ? p.l : first + p.tokens;
   // The sequence that row `first` lies in, or the first one that starts there or
   // later: the first with an end above `first`, or that starts at or after it.
+  // Halved down to 16 candidates; those are compared at once instead of one load
+  // after another.
+  auto reaches = [&](int seq) { return __ldg(p.offsets + seq + 1) > first || __ldg(p.offsets + seq) >= first; };
   int lo_seq = 0, hi_seq = p.n;
-  while (lo_seq < hi_seq) {
+  while (hi_seq - lo_seq > 16) {
     const int mid = (lo_seq + hi_seq) >> 1;
-    if (__ldg(p.offsets + mid + 1) > first || __ldg(p.offsets + mid) >= first) hi_seq = mid;
+    if (reaches(mid)) hi_seq = mid;
     else lo_seq = mid + 1;
   }
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) before += lo_seq + i < hi_seq && !reaches(lo_seq + i);
+  lo_seq += before;
   if (lo_seq >= p.n) return;
   const Walk<T, K, V, VEC> walk(p, ch);
   for (int seq = lo_seq; seq < p.n; ++seq) {
@@ -184,10 +284,10 @@ struct StepArgs {
 
 template <typename T, int K, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(const StepArgs p) {
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long seq = id / p.groups;
-  if (seq >= p.n) return;
-  const int ch = (int)(id - seq * p.groups) * V;
+  int place;
+  long long seq;
+  if (!my_place(p.groups, &place, &seq) || seq >= p.n) return;
+  const int ch = place * V;
   const int slot = slot_of(p.slots, (int)seq, p.state_slots);
   if (slot < 0) return;
   T* state = static_cast<T*>(p.state) + (long long)slot * (K - 1) * p.c + ch;
@@ -216,32 +316,46 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(const StepAr
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Launch over `groups` channel vectors x `items`, kept to whole rows of blocks with
+// few idle threads; `bytes` of shared memory a thread.
+template <typename Args>
+cudaError_t launch(void (*kernel)(const Args), const Args& p, int groups, long long items, int bytes, cudaStream_t s) {
+  const int gx = (groups + kThreads - 1) / kThreads, bx = (groups + gx - 1) / gx, by = kThreads / bx;
+  const long long gy = (items + by - 1) / by, y = gy < 32768 ? gy : 32768, z = (gy + y - 1) / y;
+  if (z > 65535) return cudaErrorInvalidConfiguration;
+  kernel<<<dim3((unsigned)gx, (unsigned)y, (unsigned)z), dim3(bx, by), bx * by * bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+constexpr long long kFullThreads = 148 * 324;   // threads that fill the device
+
 template <typename T, int K>
 cudaError_t conv_typed(ConvArgs p, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  p.tiles = p.l > 0 ? (p.l - 1) / kTokens + 1 : 1;   // without rows there are still windows to write
+  constexpr int V = kBytes / sizeof(T);
   const bool vec = on16(p.x) && on16(p.w) && on16(p.out) && on16(p.state) && on16(p.bias) && p.c % V == 0 && p.x_sn % V == 0 &&
                    p.x_st % V == 0 && p.o_sn % V == 0 && p.o_st % V == 0;
   p.groups = vec ? p.c / V : p.c;
-  const long long walks = p.offsets ? p.tiles : (long long)p.n * p.tiles;
-  const long long blocks = (walks * p.groups + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (vec) causal_conv_kernel<T, K, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  else causal_conv_kernel<T, K, 1, false><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  // Long walks read the taps and the rows before them less often (64 rows: 51 us for
+  // 4 x 4096 rows of 4096 bf16 channels, 16 rows: 60 us); short ones give a small
+  // call's threads to more SMs (5120 rows of 1280: 12.0 us with 16 rows, 19.9 with 64).
+  long long walks = 0;
+  for (p.tokens = 64;; p.tokens /= 2) {
+    p.tiles = p.l > 0 ? (p.l - 1) / p.tokens + 1 : 1;   // without rows there are still windows to write
+    walks = p.offsets ? p.tiles : (long long)p.n * p.tiles;
+    if (p.tokens == 8 || walks * p.groups >= kFullThreads) break;
+  }
+  return vec ? launch(causal_conv_kernel<T, K, V, true>, p, p.groups, walks, kAhead * kBytes, s)
+             : launch(causal_conv_kernel<T, K, 1, false>, p, p.groups, walks, 0, s);
 }
 
 template <typename T, int K>
 cudaError_t step_typed(StepArgs p, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = kBytes / sizeof(T);
   const bool vec = on16(p.x) && on16(p.w) && on16(p.out) && on16(p.state) && on16(p.bias) && p.c % V == 0 && p.x_sn % V == 0 &&
                    p.o_sn % V == 0;
   p.groups = vec ? p.c / V : p.c;
-  const long long blocks = ((long long)p.n * p.groups + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (vec) causal_conv_step_kernel<T, K, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  else causal_conv_step_kernel<T, K, 1, false><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return vec ? launch(causal_conv_step_kernel<T, K, V, true>, p, p.groups, p.n, 0, s)
+             : launch(causal_conv_step_kernel<T, K, 1, false>, p, p.groups, p.n, 0, s);
 }
 
 // f(K) for the tap counts of the two operators, 2 .. 8.

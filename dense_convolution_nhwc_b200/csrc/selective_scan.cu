@@ -47,13 +47,6 @@ struct ScanArgs {
   int x_v, dt_v, z_v, b_v, c_v, out_v;   // bytes an access: 16, 8, 4, or 0 for single elements
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-template <int N>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src));
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
-}
-
 // Copies tiles of kRows x cols elements (cols <= kCols) of a tensor's consecutive
 // rows into shared rows kPitch elements apart, by all threads.  `bytes`: an access
 // (16, 8, 4, or 0 for single elements), cols and every address multiples of it.
@@ -183,9 +176,13 @@ __device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[kStates])
 // The sums over a channel's lanes of kCount tokens' y: at each step a lane passes on
 // one half of its tokens and adds its partner's share of the other, so that lane l
 // ends with tokens l * kOwn .. of the group in y[0 .. kOwn - 1].
+// With fewer tokens than lanes the last steps add the same token's shares.
 template <int kOff, int kCount, int kAll>
 __device__ __forceinline__ void reduce_lanes(float (&y)[kAll], int lane) {
-  if constexpr (kOff > 0) {
+  if constexpr (kOff > 0 && kCount == 1) {
+    y[0] += __shfl_xor_sync(0xffffffffu, y[0], kOff);
+    reduce_lanes<kOff / 2, 1>(y, lane);
+  } else if constexpr (kOff > 0) {
     const bool upper = lane & kOff;
 #pragma unroll
     for (int i = 0; i < kCount / 2; ++i) {
@@ -477,60 +474,107 @@ struct StepArgs {
   void* out;
   int n, channels, states, groups, state_slots, softplus;
   long long x_s, dt_s, z_s, b_s, c_s, out_s;
+  int bc_vec;                  // b and c in accesses of four states
 };
 
-// Bound by the states, 8 bytes a state moved.  kLanes lanes a channel, four
-// neighbouring states a lane and turn (one 16-byte access with VEC), reduced
-// over the lanes by shuffles.
-template <typename T, int kLanes, bool VEC>
+// Bound by the states, 8 bytes a state moved.  A block works on one sequence.  kLanes
+// lanes share a channel, four neighbouring states a lane and turn (one 16-byte
+// access with VEC), and go through kMine channels together: b and c are loaded and
+// converted once for them, each lane prepares and finishes one channel's token
+// (delta and the gate), and that many loads are in flight.  One channel at a time
+// took 260 instructions for four states, mostly addresses and the softplus.
+template <typename T, int kLanes, int kMine, bool VEC>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
-  const long long id = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
+  constexpr int kAcross = 32 / kLanes, kSub = kLanes / kMine;   // channels side by side; lanes that hold one channel's token
+  const int seq = blockIdx.z * gridDim.y + blockIdx.y;
+  if (seq >= p.n) return;
+  const int slot = slot_of(p.slots, seq, p.state_slots);
+  if (slot < 0) return;
   const int lane = threadIdx.x % kLanes;
-  const bool live = id < (long long)p.n * p.channels;
-  const int seq = live ? (int)(id / p.channels) : 0;
-  const int ch = live ? (int)(id - (long long)seq * p.channels) : 0;
-  const int slot = live ? slot_of(p.slots, seq, p.state_slots) : -1;
-  float y = 0.0f, xv = 0.0f;
-  if (slot >= 0) {
-    const int group = ch / (p.channels / p.groups);
-    float* state = p.state + ((long long)slot * p.channels + ch) * p.states;
-    const float* a = p.a + (long long)ch * p.states;
-    const T* b = static_cast<const T*>(p.b) + seq * p.b_s + group * p.states;
-    const T* c = static_cast<const T*>(p.c) + seq * p.c_s + group * p.states;
-    xv = ld_f32(static_cast<const T*>(p.x) + seq * p.x_s + ch);
-    float delta = ld_f32(static_cast<const T*>(p.dt) + seq * p.dt_s + ch) + (p.dt_bias ? __ldg(p.dt_bias + ch) : 0.0f);
-    if (p.softplus) delta = softplus(delta);
-    const float dx = delta * xv, de2 = delta * kLog2e;
-    for (int s = lane * 4; s < p.states; s += kLanes * 4) {
-      if constexpr (VEC) {
-        float4 h = *reinterpret_cast<const float4*>(state + s);
-        const float4 av = __ldg(reinterpret_cast<const float4*>(a + s));
-        h.x = fmaf(decay(av.x, de2), h.x, dx * ld_f32(b + s));
-        h.y = fmaf(decay(av.y, de2), h.y, dx * ld_f32(b + s + 1));
-        h.z = fmaf(decay(av.z, de2), h.z, dx * ld_f32(b + s + 2));
-        h.w = fmaf(decay(av.w, de2), h.w, dx * ld_f32(b + s + 3));
-        y = fmaf(ld_f32(c + s), h.x, y);
-        y = fmaf(ld_f32(c + s + 1), h.y, y);
-        y = fmaf(ld_f32(c + s + 2), h.z, y);
-        y = fmaf(ld_f32(c + s + 3), h.w, y);
-        *reinterpret_cast<float4*>(state + s) = h;
+  const int first = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kAcross * kMine + threadIdx.x % 32 / kLanes;
+  const int mine = first + lane / kSub * kAcross;
+  float xv = 0.0f, delta = 0.0f, skip = 0.0f, gate = 1.0f;
+  if (mine < p.channels) {
+    xv = ld_f32(static_cast<const T*>(p.x) + seq * p.x_s + mine);
+    delta = ld_f32(static_cast<const T*>(p.dt) + seq * p.dt_s + mine);
+    if (p.z) gate = ld_f32(static_cast<const T*>(p.z) + seq * p.z_s + mine);
+    if (p.dt_bias) delta += __ldg(p.dt_bias + mine);
+    if (p.d) skip = __ldg(p.d + mine);
+  }
+  // with several channels a turn they are all of one group
+  const int group = p.groups > 1 ? min(first, p.channels - 1) / (p.channels / p.groups) : 0;
+  const T* b = static_cast<const T*>(p.b) + seq * p.b_s + group * p.states;
+  const T* c = static_cast<const T*>(p.c) + seq * p.c_s + group * p.states;
+  float* state = p.state + (long long)slot * p.channels * p.states;
+  float de2[kMine], dx[kMine], y[kMine];
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) y[q] = 0.0f;
+  bool ready = false;
+  for (int s = lane * 4; s < (p.states + 3) / 4 * 4 || !ready; s += kLanes * 4) {
+    const int have = min(max(p.states - s, 0), 4);
+    float av[kMine][4], h[kMine][4], bv[4], cv[4];
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int ch = min(first + q * kAcross, p.channels - 1);
+      const float *hp = state + (long long)ch * p.states + s, *ap = p.a + (long long)ch * p.states + s;
+      if (VEC && have == 4) {
+        load_f32<float, 4, true>(hp, h[q]);
+        load_f32<float, 4, true>(ap, av[q]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (s + i >= p.states) break;
-          const float h = fmaf(decay(__ldg(a + s + i), de2), state[s + i], dx * ld_f32(b + s + i));
-          y = fmaf(ld_f32(c + s + i), h, y);
-          state[s + i] = h;
+          h[q][i] = i < have ? hp[i] : 0.0f;
+          av[q][i] = i < have ? __ldg(ap + i) : 0.0f;
+        }
+      }
+    }
+    if (p.bc_vec && have == 4) {
+      load_f32<T, 4, true>(b + s, bv);
+      load_f32<T, 4, true>(c + s, cv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bv[i] = i < have ? ld_f32(b + s + i) : 0.0f;
+        cv[i] = i < have ? ld_f32(c + s + i) : 0.0f;
+      }
+    }
+    if (!ready) {                 // behind the loads' issue: they do not wait for it
+      ready = true;
+      if (p.softplus) delta = softplus(delta);
+      const float mine_de2 = delta * kLog2e, mine_dx = delta * xv;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        de2[q] = __shfl_sync(0xffffffffu, mine_de2, q * kSub, kLanes);
+        dx[q] = __shfl_sync(0xffffffffu, mine_dx, q * kSub, kLanes);
+      }
+    }
+    if (have == 0) continue;      // nothing of a lane past the states enters the sums, not even 0 * inf
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!VEC && i >= have) break;
+        h[q][i] = fmaf(decay(av[q][i], de2[q]), h[q][i], dx[q] * bv[i]);
+        y[q] = fmaf(cv[i], h[q][i], y[q]);
+      }
+      if (first + q * kAcross < p.channels) {
+        float* hp = state + (long long)(first + q * kAcross) * p.states + s;
+        if (VEC && have == 4) {
+          store_f32<float, 4, true>(hp, h[q]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < have) hp[i] = h[q][i];
         }
       }
     }
   }
-#pragma unroll
-  for (int off = 1; off < kLanes; off *= 2) y += __shfl_xor_sync(0xffffffffu, y, off);
-  if (slot >= 0 && lane == 0) {
-    if (p.d) y = fmaf(__ldg(p.d + ch), xv, y);
-    if (p.z) y *= silu(ld_f32(static_cast<const T*>(p.z) + seq * p.z_s + ch));
-    st_f32(static_cast<T*>(p.out) + seq * p.out_s + ch, y);
+  reduce_lanes<kLanes / 2, kMine>(y, lane);
+  if (lane % kSub == 0 && mine < p.channels) {
+    float v = y[0];
+    if (p.d) v = fmaf(skip, xv, v);
+    if (p.z) v *= silu(gate);
+    st_f32(static_cast<T*>(p.out) + seq * p.out_s + mine, v);
   }
 }
 
@@ -592,24 +636,40 @@ cudaError_t scan_typed(const ScanArgs& p, const ScanPlan& plan, cudaStream_t s) 
   return cudaErrorInvalidValue;
 }
 
+constexpr int kStepMine = 4;
+constexpr long long kManySteps = 148 * 2 * kThreads;   // threads
+
 template <typename T>
-cudaError_t step_typed(const StepArgs& p, cudaStream_t s) {
+cudaError_t step_typed(StepArgs p, cudaStream_t s) {
   const bool vec = ((reinterpret_cast<uintptr_t>(p.state) | reinterpret_cast<uintptr_t>(p.a)) & 15) == 0 && p.states % 4 == 0;
+  p.bc_vec = ((reinterpret_cast<uintptr_t>(p.b) | reinterpret_cast<uintptr_t>(p.c)) & (4 * sizeof(T) - 1)) == 0 &&
+             p.b_s % 4 == 0 && p.c_s % 4 == 0 && p.states % 4 == 0;
   int lanes = 1;
   while (lanes * 4 < p.states && lanes < 32) lanes *= 2;
-  const long long blocks = ((long long)p.n * p.channels * lanes + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto run = [&](auto kernel) {
-    kernel<<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+  // Several channels a turn where that still leaves every SM a few blocks, and where a
+  // warp's channels share b and c.
+  int mine = lanes < kStepMine ? lanes : kStepMine;
+  const int together = 32 / lanes * mine;
+  if ((long long)p.n * p.channels * lanes / mine < kManySteps || (p.groups > 1 && p.channels / p.groups % together != 0)) mine = 1;
+  const int across = kThreads / lanes * mine, y = p.n < 32768 ? p.n : 32768;
+  const dim3 grid((p.channels + across - 1) / across, y, (unsigned)((p.n + y - 1LL) / y));
+  if (grid.z > 65535) return cudaErrorInvalidConfiguration;
+  auto with = [&](auto l) {
+    auto run = [&](auto kernel) {
+      kernel<<<grid, kThreads, 0, s>>>(p);
+      return cudaGetLastError();
+    };
+    constexpr int kMine = l() < kStepMine ? l() : kStepMine;
+    if (mine > 1) return vec ? run(scan_step_kernel<T, l(), kMine, true>) : run(scan_step_kernel<T, l(), kMine, false>);
+    return vec ? run(scan_step_kernel<T, l(), 1, true>) : run(scan_step_kernel<T, l(), 1, false>);
   };
   switch (lanes) {
-    case 1: return vec ? run(scan_step_kernel<T, 1, true>) : run(scan_step_kernel<T, 1, false>);
-    case 2: return vec ? run(scan_step_kernel<T, 2, true>) : run(scan_step_kernel<T, 2, false>);
-    case 4: return vec ? run(scan_step_kernel<T, 4, true>) : run(scan_step_kernel<T, 4, false>);
-    case 8: return vec ? run(scan_step_kernel<T, 8, true>) : run(scan_step_kernel<T, 8, false>);
-    case 16: return vec ? run(scan_step_kernel<T, 16, true>) : run(scan_step_kernel<T, 16, false>);
-    default: return vec ? run(scan_step_kernel<T, 32, true>) : run(scan_step_kernel<T, 32, false>);
+    case 1: return with(std::integral_constant<int, 1>{});
+    case 2: return with(std::integral_constant<int, 2>{});
+    case 4: return with(std::integral_constant<int, 4>{});
+    case 8: return with(std::integral_constant<int, 8>{});
+    case 16: return with(std::integral_constant<int, 16>{});
+    default: return with(std::integral_constant<int, 32>{});
   }
 }
 

@@ -27,6 +27,13 @@ __device__ __forceinline__ int slot_of(const int* slots, int seq, int state_slot
   return (unsigned)v < (unsigned)state_slots ? v : -1;
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src));
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N));
+}
+
 // V elements as fp32.  VEC: one aligned access of V * sizeof(T) bytes (16 at
 // most); else V accesses of one element.
 template <typename T, int V, bool VEC>
@@ -56,6 +63,11 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
     raw.z = pack2<T>(v[4], v[5]);
     raw.w = pack2<T>(v[6], v[7]);
     *reinterpret_cast<uint4*>(p) = raw;
+  } else if constexpr (VEC && sizeof(T) == 2 && V == 4) {
+    uint2 raw;
+    raw.x = pack2<T>(v[0], v[1]);
+    raw.y = pack2<T>(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = raw;
   } else if constexpr (VEC && sizeof(T) == 4 && V == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {

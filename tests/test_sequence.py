@@ -17,10 +17,15 @@ B200 = B.DeviceProps(148, 10, 0, 183359 * 2 ** 20)
 
 # ------------------------------ no GPU needed ----------------------------------
 
+def flat(fields):
+    """Field values, a stride array's elements as values of their own."""
+    return [v for f in fields.values() for v in (f if isinstance(f, tuple) else (f,))]
+
+
 def conv_desc(**over):
     d = dict(n=2, l=5, c=8, k=4, activation=0, carry=1, state_slots=2, x_stride=(40, 8), out_stride=(40, 8))
     d.update(over)
-    return B.CausalConvDesc(*d.values())
+    return B.CausalConvDesc(*flat(d))
 
 
 # distinct, aligned addresses that no refused call may touch
@@ -60,7 +65,7 @@ def scan_desc(**over):
     d = dict(n=2, l=5, d=8, s=16, groups=2, softplus=1, carry=1, state_slots=2, x_stride=(40, 8), dt_stride=(40, 8),
              z_stride=(40, 8), b_stride=(160, 32), c_stride=(160, 32), out_stride=(40, 8))
     d.update(over)
-    return B.ScanDesc(*d.values())
+    return B.ScanDesc(*flat(d))
 
 
 def scan_tensors(**over):
