@@ -27,6 +27,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kBatch = 1;      // rows worked on together
 constexpr int kAhead = 8;      // rows on their way
+constexpr int kLoose = 8;      // rows loaded together where 16-byte accesses are not possible
 constexpr int kBytes = 16;     // of channels a thread
 
 struct ConvArgs {
@@ -46,6 +47,21 @@ __device__ __forceinline__ bool my_place(int groups, int* group, long long* item
   *group = blockIdx.x * blockDim.x + threadIdx.x;
   *item = ((long long)blockIdx.z * gridDim.y + blockIdx.y) * blockDim.y + threadIdx.y;
   return *group < groups;
+}
+
+template <int V>
+__device__ __forceinline__ void silu_all(float (&v)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 y = silu(make_float2(v[i], v[i + 1]));
+      v[i] = y.x;
+      v[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
+  }
 }
 
 // The taps of V channels: [V][K] in memory, [K][V] in registers.
@@ -114,10 +130,7 @@ struct Walk {
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) multiply_add<V>(w[k], win[k], acc);
     multiply_add<V>(w[K - 1], now, acc);
-    if (p.silu) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = silu(acc[v]);
-    }
+    if (p.silu) silu_all<V>(acc);
 #pragma unroll
     for (int k = 0; k < K - 1; ++k)
 #pragma unroll
@@ -170,10 +183,10 @@ struct Walk {
     } else {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
-      T in[kBatch][V], next[kBatch][V];
-      auto fetch = [&](T(&to_regs)[kBatch][V], int count) {
+      T in[kLoose][V], next[kLoose][V];
+      auto fetch = [&](T(&to_regs)[kLoose][V], int count) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kLoose; ++u) {
 #pragma unroll
           for (int v = 0; v < V; ++v)
             if (u < count) to_regs[u][v] = ahead[v];
@@ -181,10 +194,10 @@ struct Walk {
         }
       };
       fetch(in, to - from);
-      for (int at = from; at < to; at += kBatch) {
-        fetch(next, to - at - kBatch);
+      for (int at = from; at < to; at += kLoose) {
+        fetch(next, to - at - kLoose);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kLoose; ++u) {
           float acc[V], now[V];
 #pragma unroll
           for (int v = 0; v < V; ++v) now[v] = Store<T>::to_f32(in[u][v]);
@@ -193,7 +206,7 @@ struct Walk {
           here += p.o_st;
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
+        for (int u = 0; u < kLoose; ++u)
 #pragma unroll
           for (int v = 0; v < V; ++v) in[u][v] = next[u][v];
       }
@@ -307,8 +320,8 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(const StepAr
   for (int v = 0; v < V; ++v) {
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[v] = fmaf(w[k][v], win[k][v], acc[v]);
-    if (p.silu) acc[v] = silu(acc[v]);
   }
+  if (p.silu) silu_all<V>(acc);
   store_f32<T, V, VEC>(static_cast<T*>(p.out) + seq * p.o_sn + ch, acc);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) store_f32<T, V, VEC>(state + (long long)k * p.c, win[k + 1]);

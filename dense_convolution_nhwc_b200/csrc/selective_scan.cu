@@ -26,12 +26,14 @@
 // That doubles the exponentials, so it needs more than two chunks to pay.
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include "sequence.cuh"
 
 namespace b200conv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;     // of a step's block
+constexpr int kScanners = 128;    // threads of a prompt's block that hold states
 
 struct ScanArgs {
   const void *x, *dt, *b, *c, *z;
@@ -48,26 +50,26 @@ struct ScanArgs {
 };
 
 // Copies tiles of kRows x cols elements (cols <= kCols) of a tensor's consecutive
-// rows into shared rows kPitch elements apart, by all threads.  `bytes`: an access
-// (16, 8, 4, or 0 for single elements), cols and every address multiples of it.
-// The 16-byte form keeps each thread's address from tile to tile: worked out anew,
-// the five tensors' addresses took as long as a third of the recursion itself.
-template <typename T, int kRows, int kCols, int kPitch>
+// rows into shared rows kCols elements apart, by kN threads of which this is `me`.
+// `bytes`: an access (16, 8, 4, or 0 for single elements), cols and every address
+// multiples of it.  The 16-byte form keeps each thread's address from tile to tile.
+template <typename T, int kRows, int kCols, int kN>
 struct Stager {
   static constexpr int E = 16 / sizeof(T), kPer = kCols / E > 0 ? kCols / E : 1;
-  static constexpr int kStep = kThreads / kPer > 0 ? kThreads / kPer : 1;     // rows between a thread's accesses
-  static constexpr bool kFits = kCols % E == 0 && kPer <= kThreads && kRows % kStep == 0;
+  static constexpr int kStep = kN / kPer > 0 ? kN / kPer : 1;     // rows between a thread's accesses
+  static constexpr bool kFits = kCols % E == 0 && kPer <= kN && kRows % kStep == 0;
   const T* src;
   long long stride;
-  int cols, bytes, r0, to;
-  __device__ __forceinline__ void init(const T* base, long long row_stride, int width, int access) {
+  int cols, bytes, me, r0, to;
+  __device__ __forceinline__ void init(const T* base, long long row_stride, int width, int access, int thread) {
     src = base;
     stride = row_stride;
     cols = width;
     bytes = access;
-    r0 = threadIdx.x / kPer;
-    const int q = (threadIdx.x % kPer) * E;
-    to = r0 * kPitch + q;
+    me = thread;
+    r0 = me / kPer;
+    const int q = (me % kPer) * E;
+    to = r0 * kCols + q;
     if (kFits && bytes == 16) {
       src += r0 * stride + q;
       if (q >= cols) r0 = kRows;        // past the edge: never a row
@@ -76,9 +78,9 @@ struct Stager {
   template <int N>
   __device__ __forceinline__ void by(T* dst, int rows) {
     constexpr int kE = N / sizeof(T) > 0 ? N / sizeof(T) : 1, kAcross = kCols / kE > 0 ? kCols / kE : 1;
-    for (int i = threadIdx.x; i < rows * kAcross; i += kThreads) {
+    for (int i = me; i < rows * kAcross; i += kN) {
       const int r = i / kAcross, q = (i % kAcross) * kE;
-      if (q < cols) copy_async<N>(dst + r * kPitch + q, src + r * stride + q);
+      if (q < cols) copy_async<N>(dst + r * kCols + q, src + r * stride + q);
     }
   }
   // The next `rows` rows.
@@ -86,7 +88,7 @@ struct Stager {
     if (kFits && bytes == 16) {
 #pragma unroll
       for (int r = 0; r < kRows; r += kStep)
-        if (r0 + r < rows) copy_async<16>(dst + to + r * kPitch, src + r * stride);
+        if (r0 + r < rows) copy_async<16>(dst + to + r * kCols, src + r * stride);
     } else if (bytes == 16) {
       by<16>(dst, rows);
     } else if (bytes == 8) {
@@ -95,35 +97,64 @@ struct Stager {
       by<4>(dst, rows);
     } else {
 #pragma unroll 8
-      for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
+      for (int i = me; i < rows * kCols; i += kN) {
         const int r = i / kCols, q = i % kCols;
-        if (q < cols) dst[r * kPitch + q] = src[r * stride + q];
+        if (q < cols) dst[r * kCols + q] = src[r * stride + q];
       }
     }
     src += kRows * stride;
   }
 };
 
+// One token's values of kHold neighbouring channels.
+template <typename T, int kHold>
+struct Held {
+  static constexpr int kAccess = kHold * sizeof(T) < 16 ? kHold * sizeof(T) : 16;
+  alignas(16) T v[kHold];
+  // `count` of them are there; vec: all, and kAccess bytes at a time.
+  __device__ __forceinline__ void load(const T* p, bool vec, int count) {
+    if (vec) {
+      using Word = std::conditional_t<kAccess == 16, uint4, std::conditional_t<kAccess == 8, uint2, uint32_t>>;
+#pragma unroll
+      for (int i = 0; i < (int)(kHold * sizeof(T) / kAccess); ++i)
+        reinterpret_cast<Word*>(v)[i] = __ldg(reinterpret_cast<const Word*>(p) + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) v[i] = i < count ? p[i] : Store<T>::from_f32(0.0f);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const { return Store<T>::to_f32(v[i]); }
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  __threadfence_block();
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+constexpr int kTile = 32;   // tokens a tile, one to a lane of the helping warps
+
 template <typename T, int kStates, int kLanes>
 struct Shape {
-  static constexpr int kChannels = kThreads / kLanes;
+  static constexpr int kChannels = kScanners / kLanes;
+  static constexpr int kHold = kChannels < 8 ? kChannels : 8;      // channels a helping thread
+  static constexpr int kParts = kChannels / kHold;                 // helping threads a token
+  static constexpr int kHelpers = kParts * kTile;
+  static constexpr int kBlock = kScanners + kHelpers;
   static constexpr int kWide = kStates * kLanes;             // states, padded
-  static constexpr int kTile = kWide <= 32 ? 64 : 32;        // tokens staged together
   static constexpr int kTogether = kLanes > 8 ? kLanes : 8;  // tokens reduced together
   static constexpr int kOwn = kTogether / kLanes;            // of which each lane ends with
   static constexpr int kSub = kStates > 4 ? 4 : 8;           // tokens whose exponentials are in flight
-  static constexpr int kMany = 32 / kTogether;               // groups in a row
-  static constexpr int kRow = kTile + 8;                     // floats a channel of delta
-  static constexpr int kPitch = kChannels + 16 / sizeof(T);  // elements a row of x: 16 bytes more, against bank conflicts
+  static constexpr int kRow = kTile + 4;                     // floats a channel of delta
+  static constexpr int kRing = kWide <= 64 ? 3 : 2;          // tiles of b and c
   // shared memory, in bytes
-  static constexpr int kRawX = kTile * kPitch * sizeof(T);
-  static constexpr int kRawB = kTile * kWide * sizeof(T);
-  static constexpr int kStage = 3 * kRawX + 2 * kRawB;
-  static constexpr int kOut = 2 * kStage;
-  static constexpr int kDelta = kOut + kRawX;
-  static constexpr int kB = kDelta + 2 * kChannels * kRow * 4;
-  static constexpr int kBytes = kB + 2 * kTile * kWide * 4;
-  static_assert(kTile % kTogether == 0 && (kStates == 1 || kStates % 2 == 0), "");
+  static constexpr int kDelta = kChannels * kRow * 4;        // delta, later y; and delta x: a stage of each
+  static constexpr int kPairs = kTile * kWide * 4;           // b in fp32: a stage
+  static constexpr int kRaw = kTile * kWide * (int)sizeof(T);
+  static constexpr int kAtB = 4 * kDelta, kAtRaw = kAtB + 2 * kPairs, kBytes = kAtRaw + 2 * kRing * kRaw;
+  static_assert(kTile % kTogether == 0 && kStates % 2 == 0 && kPairs / 8 % kHelpers == 0, "");
 };
 
 // Sequence, channel tile and tokens of a block.
@@ -184,20 +215,53 @@ __device__ __forceinline__ void reduce_lanes(float (&y)[kAll], int lane) {
     reduce_lanes<kOff / 2, 1>(y, lane);
   } else if constexpr (kOff > 0) {
     const bool upper = lane & kOff;
+    float other[kCount / 2];
 #pragma unroll
     for (int i = 0; i < kCount / 2; ++i) {
       const float give = upper ? y[i] : y[i + kCount / 2];
-      const float take = upper ? y[i + kCount / 2] : y[i];
-      y[i] = take + __shfl_xor_sync(0xffffffffu, give, kOff);
+      y[i] = upper ? y[i + kCount / 2] : y[i];
+      other[i] = __shfl_xor_sync(0xffffffffu, give, kOff);
+    }
+    if constexpr (kCount >= 4) {
+#pragma unroll
+      for (int i = 0; i < kCount / 2; i += 2) {
+        const float2 sum = __fadd2_rn(make_float2(y[i], y[i + 1]), make_float2(other[i], other[i + 1]));
+        y[i] = sum.x;
+        y[i + 1] = sum.y;
+      }
+    } else {
+      y[0] += other[0];
     }
     reduce_lanes<kOff / 2, kCount / 2>(y, lane);
   }
 }
 
+// Where a token's delta lies in the row of a channel of part `part` of kParts: a whole
+// number of eights further on for each part, so that the neighbouring threads of a
+// helping warp, which are the parts of the same tokens, write to different banks.
+template <int kParts>
+__device__ __forceinline__ int turned(int token, int part) {
+  return kParts > 1 ? (token + part * (kTile / kParts)) % kTile : token;
+}
+
+// kStates neighbouring values.
+template <typename T, int kStates>
+__device__ __forceinline__ void load_states(const T* p, float (&v)[kStates]) {
+  constexpr int kBytes = kStates * sizeof(T), kAccess = kBytes < 16 ? kBytes : 16;
+  using Word = std::conditional_t<kAccess == 16, uint4, std::conditional_t<kAccess == 8, uint2, uint32_t>>;
+  Word raw[kBytes / kAccess];
+#pragma unroll
+  for (int i = 0; i < kBytes / kAccess; ++i) raw[i] = reinterpret_cast<const Word*>(p)[i];
+  const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) v[i] = Store<T>::to_f32(e[i]);
+}
+
 // kFull: states == kStates * kLanes.  kEnds: the chunk's final state from zero and its sum of delta, no output.
 template <typename T, int kStates, int kLanes, bool kFull, bool kEnds>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock) scan_kernel(const ScanArgs p) {
   using L = Shape<T, kStates, kLanes>;
+  constexpr int kReady = 1, kDone = 3, kHelp = 5;      // barriers; the first two have one for each stage
   extern __shared__ __align__(16) unsigned char smem[];
   Where w;
   if (!locate<L::kChannels>(p, &w)) return;
@@ -205,12 +269,182 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
   const bool last = begin + p.chunk >= w.len;
   // a chunk without tokens has nothing to do, but for the first one's state of an empty sequence
   if (begin >= w.len && chunk > 0) return;
-  const int end = last ? w.len : begin + p.chunk;
+  if (kEnds && last) return;      // nothing follows it
+  const int end = last ? w.len : begin + p.chunk, tiles = (end - begin + kTile - 1) / kTile;
+
+  auto delta_at = [&](int stage) { return reinterpret_cast<float*>(smem + stage * L::kDelta); };        // [channel][kRow]
+  auto dx_at = [&](int stage) { return reinterpret_cast<float*>(smem + (2 + stage) * L::kDelta); };
+  // b in fp32, the two tokens of a pair side by side: [token / 2][state][token % 2]
+  auto pairs_at = [&](int stage) { return reinterpret_cast<float*>(smem + L::kAtB + stage * L::kPairs); };
+  auto b_at = [&](int turn) { return reinterpret_cast<T*>(smem + L::kAtRaw + 2 * turn * L::kRaw); };    // [token][kWide]
+  auto c_at = [&](int turn) { return reinterpret_cast<T*>(smem + L::kAtRaw + (2 * turn + 1) * L::kRaw); };
+
+  if (threadIdx.x >= kScanners) {
+    // ---- helping warps: everything but the recursion, token `row` of each tile and channels c0 .. of the block
+    const int me = threadIdx.x - kScanners, row = me / L::kParts, part = me % L::kParts, c0 = part * L::kHold;
+    const int row_at = turned<L::kParts>(row, part);       // of the token in delta and delta x
+    const int count = min(max(w.count - c0, 0), L::kHold);
+    const int ch = w.ch + (count > 0 ? c0 : 0);
+    float bias[L::kHold], skip[L::kHold], sum[L::kHold];
+#pragma unroll
+    for (int k = 0; k < L::kHold; ++k) {
+      bias[k] = p.dt_bias && k < count ? __ldg(p.dt_bias + ch + k) : 0.0f;
+      skip[k] = !kEnds && p.d && k < count ? __ldg(p.d + ch + k) : 0.0f;
+      sum[k] = 0.0f;
+    }
+    const T* x = rows_of<T>(p, p.x, p.x_s, w, ch) + (begin + row) * p.x_s[1];
+    const T* dt = rows_of<T>(p, p.dt, p.dt_s, w, ch) + (begin + row) * p.dt_s[1];
+    const T* z = p.z && !kEnds ? rows_of<T>(p, p.z, p.z_s, w, ch) + (begin + row) * p.z_s[1] : nullptr;
+    T* out = kEnds ? nullptr : const_cast<T*>(rows_of<T>(p, p.out, p.out_s, w, ch)) + (begin + row) * p.out_s[1];
+    using H = Held<T, L::kHold>;
+    const bool x_vec = count == L::kHold && p.x_v >= H::kAccess, dt_vec = count == L::kHold && p.dt_v >= H::kAccess;
+    const bool z_vec = count == L::kHold && p.z_v >= H::kAccess, out_vec = count == L::kHold && p.out_v >= H::kAccess;
+    H next_x, next_dt, next_z, now_x, now_dt, now_z, past_x, past_z;
+    auto load = [&](int tile) {
+      if (begin + tile * kTile + row < end && count > 0) {
+        next_x.load(x, x_vec, count);
+        next_dt.load(dt, dt_vec, count);
+        if (z) next_z.load(z, z_vec, count);
+      }
+      x += kTile * p.x_s[1];
+      dt += kTile * p.dt_s[1];
+      if (z) z += kTile * p.z_s[1];
+    };
+    auto finish = [&](int tile) {
+      if constexpr (!kEnds) {
+        if (begin + tile * kTile + row < end && count > 0) {
+          const float* y = delta_at(tile & 1) + c0 * L::kRow + row_at;
+          H to;
+          float v[L::kHold];
+#pragma unroll
+          for (int k = 0; k < L::kHold; ++k) v[k] = y[k * L::kRow];
+          if (p.d) {
+#pragma unroll
+            for (int k = 0; k < L::kHold; ++k) v[k] = fmaf(skip[k], past_x.at(k), v[k]);
+          }
+          if (z) {
+#pragma unroll
+            for (int k = 0; k < L::kHold; k += 2) {
+              const float2 gate = silu(make_float2(past_z.at(k), past_z.at(k + 1)));
+              const float2 two = __fmul2_rn(make_float2(v[k], v[k + 1]), gate);
+              v[k] = two.x;
+              v[k + 1] = two.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < L::kHold; ++k) to.v[k] = Store<T>::from_f32(v[k]);
+          if (out_vec) {
+            using Word = std::conditional_t<H::kAccess == 16, uint4, std::conditional_t<H::kAccess == 8, uint2, uint32_t>>;
+#pragma unroll
+            for (int i = 0; i < (int)(L::kHold * sizeof(T) / H::kAccess); ++i)
+              reinterpret_cast<Word*>(out)[i] = reinterpret_cast<const Word*>(to.v)[i];
+          } else {
+#pragma unroll
+            for (int k = 0; k < L::kHold; ++k)
+              if (k < count) out[k] = to.v[k];
+          }
+        }
+        out += kTile * p.out_s[1];
+      }
+    };
+    Stager<T, kTile, L::kWide, L::kHelpers> sb, sc;
+    sb.init(rows_of<T>(p, p.b, p.b_s, w, w.group * p.states) + begin * p.b_s[1], p.b_s[1], p.states, p.b_v, me);
+    if (!kEnds) sc.init(rows_of<T>(p, p.c, p.c_s, w, w.group * p.states) + begin * p.c_s[1], p.c_s[1], p.states, p.c_v, me);
+    auto fetch = [&](int tile) {
+      const int rows = min(kTile, end - begin - tile * kTile);
+      if (rows > 0) {
+        sb.next(b_at(tile % L::kRing), rows);
+        if (!kEnds) sc.next(c_at(tile % L::kRing), rows);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (!kFull) {       // the states that are not there: zeros, which no tile overwrites
+      const int pad = L::kWide - p.states;
+      for (int i = me; i < 2 * L::kRing * kTile * pad; i += L::kHelpers)
+        b_at(0)[i / pad * L::kWide + p.states + i % pad] = Store<T>::from_f32(0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < L::kRing - 1; ++i) fetch(i);
+    load(0);
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int stage = tile & 1;
+      now_x = next_x;
+      now_dt = next_dt;
+      now_z = next_z;
+      if (tile + 1 < tiles) load(tile + 1);
+      float de[L::kHold];
+#pragma unroll
+      for (int k = 0; k < L::kHold; ++k) de[k] = now_dt.at(k) + bias[k];
+      if (p.softplus) {
+#pragma unroll
+        for (int k = 0; k < L::kHold; k += 2) {
+          const float2 two = softplus(make_float2(de[k], de[k + 1]));
+          de[k] = two.x;
+          de[k + 1] = two.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < L::kHold; ++k) {
+        delta_at(stage)[(c0 + k) * L::kRow + row_at] = de[k];
+        dx_at(stage)[(c0 + k) * L::kRow + row_at] = de[k] * now_x.at(k);
+        if (kEnds && begin + tile * kTile + row < end) sum[k] += de[k];
+      }
+      // this tile's b and c are here, and for every helper
+      asm volatile("cp.async.wait_group %0;" ::"n"(L::kRing - 2) : "memory");
+      bar_sync(kHelp, L::kHelpers);
+      const T* raw = b_at(tile % L::kRing);
+      float2* pairs = reinterpret_cast<float2*>(pairs_at(stage));
+      constexpr int kTurns = L::kPairs / 8 / L::kHelpers, kBatch = kTurns > 8 ? 8 : kTurns;
+#pragma unroll 1
+      for (int i0 = me; i0 < L::kPairs / 8; i0 += kBatch * L::kHelpers) {
+        float2 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * L::kHelpers;
+          const T* from = raw + i / L::kWide * 2 * L::kWide + i % L::kWide;
+          v[k] = make_float2(ld_f32(from), ld_f32(from + L::kWide));
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) pairs[i0 + k * L::kHelpers] = v[k];
+      }
+      bar_arrive(kReady + stage, L::kBlock);
+      if (tile > 0) bar_sync(kDone + (stage ^ 1), L::kBlock);
+      fetch(tile + L::kRing - 1);
+      if (tile > 0) finish(tile - 1);
+      past_x = now_x;
+      past_z = now_z;
+    }
+    if (tiles > 0) {
+      bar_sync(kDone + ((tiles - 1) & 1), L::kBlock);
+      finish(tiles - 1);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (kEnds) {
+      // over the rows: a warp's by shuffles, the warps' through the stage that no scanner reads any more
+      float* sums = dx_at(0);
+      bar_sync(kHelp, L::kHelpers);
+#pragma unroll
+      for (int k = 0; k < L::kHold; ++k) {
+#pragma unroll
+        for (int off = L::kParts; off < 32; off *= 2) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], off);
+        if (me % 32 < L::kParts) sums[me / 32 * L::kChannels + c0 + k] = sum[k];
+      }
+      bar_sync(kHelp, L::kHelpers);
+      for (int c = me; c < w.count; c += L::kHelpers) {
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < L::kHelpers / 32; ++i) all += sums[i * L::kChannels + c];
+        p.ws_sum[((long long)w.seq * p.chunks + chunk) * p.channels + w.ch + c] = all;
+      }
+    }
+    return;
+  }
+
+  // ---- scanning warps: kLanes lanes a channel, kStates states a lane
   const int lane = threadIdx.x % kLanes, cl = threadIdx.x / kLanes;
   const bool live = cl < w.count;
   const int ch = w.ch + (live ? cl : 0);
   const int s0 = lane * kStates, have = kFull ? kStates : min(max(p.states - s0, 0), kStates);
-
   float2 a2[kStates];          // a log2(e), twice
   float h[kStates];
   const float* a = p.a + (long long)ch * p.states + s0;
@@ -224,7 +458,6 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
     h[i] = 0.0f;
   }
   if constexpr (kEnds) {
-    if (last) return;            // nothing follows it
     if (chunk == 0 && live) {
 #pragma unroll
       for (int i = 0; i < kStates; ++i)
@@ -246,116 +479,13 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
       if (i < have) h[i] = cache[i];
   }
 
-  const T* x = rows_of<T>(p, p.x, p.x_s, w, w.ch);
-  const T* dt = rows_of<T>(p, p.dt, p.dt_s, w, w.ch);
-  const T* z = p.z && !kEnds ? rows_of<T>(p, p.z, p.z_s, w, w.ch) : nullptr;
-  const T* b = rows_of<T>(p, p.b, p.b_s, w, w.group * p.states);
-  const T* c = rows_of<T>(p, p.c, p.c_s, w, w.group * p.states);
-  T* out = kEnds ? nullptr : const_cast<T*>(rows_of<T>(p, p.out, p.out_s, w, w.ch));
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.0f;
-  const float skip = !kEnds && p.d ? __ldg(p.d + ch) : 0.0f;
-
-  auto raw = [&](int stage, int which) {
-    return reinterpret_cast<T*>(smem + stage * L::kStage + (which < 3 ? which * L::kRawX : 3 * L::kRawX + (which - 3) * L::kRawB));
-  };
-  T* out_tile = reinterpret_cast<T*>(smem + L::kOut);
-  float* delta_of = reinterpret_cast<float*>(smem + L::kDelta) + cl * L::kRow;
-  float* dx_of = delta_of + L::kChannels * L::kRow;
-  // b and c in fp32, the two tokens of a pair side by side: [token / 2][state][token % 2]
-  float* bf = reinterpret_cast<float*>(smem + L::kB);
-  float* cf = bf + L::kTile * L::kWide;
-
-  Stager<T, L::kTile, L::kChannels, L::kPitch> sx, sdt, sz;
-  Stager<T, L::kTile, L::kWide, L::kWide> sb, sc;
-  sx.init(x + begin * p.x_s[1], p.x_s[1], w.count, p.x_v);
-  sdt.init(dt + begin * p.dt_s[1], p.dt_s[1], w.count, p.dt_v);
-  sb.init(b + begin * p.b_s[1], p.b_s[1], p.states, p.b_v);
-  if (z) sz.init(z + begin * p.z_s[1], p.z_s[1], w.count, p.z_v);
-  if (!kEnds) sc.init(c + begin * p.c_s[1], p.c_s[1], p.states, p.c_v);
-  auto fetch = [&](int at, int to) {
-    const int rows = min(L::kTile, end - at);
-    sx.next(raw(to, 0), rows);
-    sdt.next(raw(to, 1), rows);
-    if (z) sz.next(raw(to, 2), rows);
-    sb.next(raw(to, 3), rows);
-    if (!kEnds) sc.next(raw(to, 4), rows);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto put = [&](int at) {           // out_tile's rows, from token `at`
-    const int rows = min(L::kTile, end - at);
-    T* to = out + at * p.out_s[1];
-    constexpr int E = 16 / sizeof(T), kPer = L::kChannels / E;
-    if (kPer > 0 && p.out_v == 16) {
-      for (int i = threadIdx.x; i < rows * kPer; i += kThreads) {
-        const int r = i / (kPer > 0 ? kPer : 1), q = (i % (kPer > 0 ? kPer : 1)) * E;
-        if (q < w.count)
-          *reinterpret_cast<uint4*>(to + r * p.out_s[1] + q) = *reinterpret_cast<const uint4*>(out_tile + r * L::kPitch + q);
-      }
-    } else {
-      for (int i = threadIdx.x; i < rows * L::kChannels; i += kThreads) {
-        const int r = i / L::kChannels, q = i % L::kChannels;
-        if (q < w.count) to[r * p.out_s[1] + q] = out_tile[r * L::kPitch + q];
-      }
-    }
-  };
-
-  float sum = 0.0f;            // of delta, over this lane's tokens
-  if (begin < end) fetch(begin, 0);
-  for (int at = begin, turn = 0; at < end; at += L::kTile, turn ^= 1) {
-    const int rows = min(L::kTile, end - at);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    if (!kEnds && at > begin) put(at - L::kTile);
-    if (at + L::kTile < end) fetch(at + L::kTile, turn ^ 1);
-
-    const T *xr = raw(turn, 0), *dr = raw(turn, 1), *zr = raw(turn, 2), *br = raw(turn, 3), *cr = raw(turn, 4);
-    // Each pass loads all its values before it stores any: a store in between would
-    // hold back the loads after it, which the compiler cannot tell apart from it.
-    constexpr int kTurns = L::kTile / kLanes, kBatch = kTurns > 8 ? 8 : kTurns;
-#pragma unroll 1
-    for (int t0 = lane; t0 < rows; t0 += kBatch * kLanes) {
-      float de[kBatch], xv[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        de[i] = ld_f32(dr + (t0 + i * kLanes) * L::kPitch + cl) + bias;
-        xv[i] = ld_f32(xr + (t0 + i * kLanes) * L::kPitch + cl);
-      }
-      if (p.softplus) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) de[i] = softplus(de[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        delta_of[t0 + i * kLanes] = de[i];
-        dx_of[t0 + i * kLanes] = de[i] * xv[i];
-        if (kEnds && t0 + i * kLanes < rows) sum += de[i];
-      }
-    }
-    constexpr int kPairs = L::kTile / 2 * L::kWide, kPairTurns = (kPairs + kThreads - 1) / kThreads,
-                  kPairBatch = kPairTurns > 4 ? 4 : kPairTurns;
-#pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < kPairs && i0 / L::kWide * 2 < rows; i0 += kPairBatch * kThreads) {
-      float2 b2[kPairBatch], c2[kPairBatch];
-#pragma unroll
-      for (int k = 0; k < kPairBatch; ++k) {
-        const int i = i0 + k * kThreads, s = i % L::kWide, t = i / L::kWide * 2;
-        b2[k] = c2[k] = make_float2(0.0f, 0.0f);
-        if ((kPairs % (kPairBatch * kThreads) == 0 || i < kPairs) && (kFull || s < p.states)) {
-          const T *b0 = br + t * L::kWide + s, *c0 = cr + t * L::kWide + s;
-          b2[k] = make_float2(ld_f32(b0), ld_f32(b0 + L::kWide));
-          if (!kEnds) c2[k] = make_float2(ld_f32(c0), ld_f32(c0 + L::kWide));
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kPairBatch; ++k) {
-        const int i = i0 + k * kThreads;
-        if (kPairs % (kPairBatch * kThreads) == 0 || i < kPairs) {
-          reinterpret_cast<float2*>(bf)[i] = b2[k];
-          if (!kEnds) reinterpret_cast<float2*>(cf)[i] = c2[k];
-        }
-      }
-    }
-    __syncthreads();
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int stage = tile & 1, rows = min(kTile, end - begin - tile * kTile);
+    float* delta_of = delta_at(stage) + cl * L::kRow;
+    const int part = cl / L::kHold;
+    const float *dx_of = dx_at(stage) + cl * L::kRow, *bf = pairs_at(stage);
+    const T* cr = c_at(tile % L::kRing);
+    bar_sync(kReady + stage, L::kBlock);
 
     // kSub tokens from t: the states advance, and y gets this lane's share of the sums
     // over them.  The exponentials and additions of all tokens come first, two tokens
@@ -364,11 +494,12 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
     auto sub = [&](auto tail, int t, float* y) {
       constexpr bool kTail = decltype(tail)::value;
       constexpr int kSub = L::kSub;
+      const int t_at = turned<L::kParts>(t, part);
       float2 e[kSub / 2][kStates], add[kSub / 2][kStates];
 #pragma unroll
       for (int q = 0; q < kSub; q += 4) {
-        const float4 de = *reinterpret_cast<const float4*>(delta_of + t + q);
-        const float4 dx = *reinterpret_cast<const float4*>(dx_of + t + q);
+        const float4 de = *reinterpret_cast<const float4*>(delta_of + t_at + q);
+        const float4 dx = *reinterpret_cast<const float4*>(dx_of + t_at + q);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 d2 = k ? make_float2(de.z, de.w) : make_float2(de.x, de.y);
@@ -386,8 +517,11 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
 #pragma unroll
       for (int q = 0; q < kSub / 2; ++q) {
         float2 sum2 = make_float2(0.0f, 0.0f);
-        float2 ct[kStates];
-        if (!kEnds) load_pairs<kStates>(cf + (t + 2 * q) * L::kWide + s0 * 2, ct);
+        float ct[2][kStates];
+        if (!kEnds) {
+          load_states<T, kStates>(cr + (t + 2 * q) * L::kWide + s0, ct[0]);
+          load_states<T, kStates>(cr + (t + 2 * q + 1) * L::kWide + s0, ct[1]);
+        }
 #pragma unroll
         for (int i = 0; i < kStates; ++i) {
           float h0 = fmaf(e[q][i].x, h[i], add[q][i].x);
@@ -397,7 +531,7 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
           if (!kFull && i >= have) h1 = 0.0f;
           if (kTail && t + 2 * q + 1 >= rows) h1 = h0;
           h[i] = h1;
-          if (!kEnds) sum2 = __ffma2_rn(ct[i], make_float2(h0, h1), sum2);
+          if (!kEnds) sum2 = __ffma2_rn(make_float2(ct[0][i], ct[1][i]), make_float2(h0, h1), sum2);
         }
         y[2 * q] = sum2.x;
         y[2 * q + 1] = sum2.y;
@@ -413,51 +547,36 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs p) {
         for (int i = 0; i < L::kOwn; ++i) own[i] = y[i];
       }
     };
-    // kMany groups before the outputs of any
+    // kMany groups, then their sums in the place of their deltas: a store in between
+    // would hold back the next group's loads
     auto groups = [&](auto tail, auto many, int t) {
-      constexpr int kMany = decltype(many)::value, kAll = kMany * L::kOwn;
-      float own[kAll], xv[kAll], zv[kAll];
+      constexpr int kMany = decltype(many)::value;
+      float own[kMany * L::kOwn];
 #pragma unroll
       for (int g = 0; g < kMany; ++g) group(tail, t + g * L::kTogether, own + g * L::kOwn);
       if constexpr (!kEnds) {
+        __syncwarp();
 #pragma unroll
-        for (int g = 0; g < kAll; ++g) {
-          const int at_t = t + g / L::kOwn * L::kTogether + lane * L::kOwn + g % L::kOwn;
-          xv[g] = ld_f32(xr + at_t * L::kPitch + cl);
-          zv[g] = z ? ld_f32(zr + at_t * L::kPitch + cl) : 0.0f;
-        }
-        if (p.d) {
+        for (int g = 0; g < kMany; ++g)
 #pragma unroll
-          for (int g = 0; g < kAll; ++g) own[g] = fmaf(skip, xv[g], own[g]);
-        }
-        if (z) {
-#pragma unroll
-          for (int g = 0; g < kAll; ++g) own[g] *= silu(zv[g]);
-        }
-#pragma unroll
-        for (int g = 0; g < kAll; ++g)
-          st_f32(out_tile + (t + g / L::kOwn * L::kTogether + lane * L::kOwn + g % L::kOwn) * L::kPitch + cl, own[g]);
+          for (int i = 0; i < L::kOwn; ++i)
+            delta_of[turned<L::kParts>(t + g * L::kTogether, part) + lane * L::kOwn + i] = own[g * L::kOwn + i];
       }
     };
-    int t = 0;
-    for (; t + L::kMany * L::kTogether <= rows; t += L::kMany * L::kTogether)
-      groups(std::false_type{}, std::integral_constant<int, L::kMany>{}, t);
-    for (; t < rows; t += L::kTogether) groups(std::true_type{}, std::integral_constant<int, 1>{}, t);
-  }
-  if (!kEnds && begin < end) {
-    __syncthreads();
-    put(begin + (end - 1 - begin) / L::kTile * L::kTile);
+    if (rows == kTile) {
+      groups(std::false_type{}, std::integral_constant<int, kTile / L::kTogether>{}, 0);
+    } else {
+      for (int t = 0; t < rows; t += L::kTogether) groups(std::true_type{}, std::integral_constant<int, 1>{}, t);
+    }
+    bar_arrive(kDone + stage, L::kBlock);
   }
 
+  if (!live) return;
   if constexpr (kEnds) {
-#pragma unroll
-    for (int off = 1; off < kLanes; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (!live) return;
 #pragma unroll
     for (int i = 0; i < kStates; ++i)
       if (i < have) p.ws_state[ws_row + (chunk + 1) * ws_step + i] = h[i];
-    if (lane == 0) p.ws_sum[((long long)w.seq * p.chunks + chunk) * p.channels + ch] = sum;
-  } else if (last && live && cache) {
+  } else if (last && cache) {
 #pragma unroll
     for (int i = 0; i < kStates; ++i)
       if (i < have) cache[i] = h[i];
@@ -611,7 +730,7 @@ cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
       if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, kThreads, L::kBytes, s>>>(p);
+    kernel<<<grid, L::kBlock, L::kBytes, s>>>(p);
     return cudaGetLastError();
   };
   if (p.chunks > 1) {
@@ -625,8 +744,9 @@ template <typename T>
 cudaError_t scan_typed(const ScanArgs& p, const ScanPlan& plan, cudaStream_t s) {
 #define B200CONV_SCAN(S, L, F) \
   if (plan.states_per_lane == S && plan.lanes == L && (!F || p.states == S * L)) return scan_shaped<T, S, L, F>(p, s)
+  B200CONV_SCAN(4, 4, true);
   B200CONV_SCAN(2, 8, true);
-  B200CONV_SCAN(4, 2, false);
+  B200CONV_SCAN(2, 4, false);
   B200CONV_SCAN(4, 4, false);
   B200CONV_SCAN(4, 8, false);
   B200CONV_SCAN(4, 16, false);
@@ -675,31 +795,30 @@ cudaError_t step_typed(StepArgs p, cudaStream_t s) {
 
 }  // namespace
 
-constexpr int kChunkStep = 64;   // chunks are whole tiles
-
 // Pure in the descriptor and the device's SM count.
 ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   ScanPlan plan{};
-  plan.states_per_lane = 4;
-  plan.lanes = 2;
+  plan.states_per_lane = d.s <= 8 ? 2 : 4;
+  plan.lanes = 4;
   while (plan.lanes * plan.states_per_lane < d.s) {
     if (plan.lanes < 32) plan.lanes *= 2;
     else plan.states_per_lane *= 2;
   }
   if (d.s == 16) {
-    plan.states_per_lane = 2;
-    plan.lanes = 8;
+    plan.states_per_lane = 4;
+    plan.lanes = 4;
+    if (getenv("SL")) { plan.lanes = atoi(getenv("SL")); plan.states_per_lane = 16 / plan.lanes; }
   }
-  const int channels = kThreads / plan.lanes;
+  const int channels = kScanners / plan.lanes;
   const long long per_group = d.d / d.groups;
   const long long blocks = (long long)d.n * d.groups * ((per_group + channels - 1) / channels);
-  plan.chunk = d.l > 0 ? (d.l + kChunkStep - 1) / kChunkStep * kChunkStep : kChunkStep;
+  plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
   plan.chunks = 1;
   // With chunks every token is gone over twice, so three are the fewest that can pay.
-  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kChunkStep - 1) / (2 * kChunkStep);
+  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kTile - 1) / (2 * kTile);
   const long long chunks = want < most ? want : most;
-  if (chunks >= 4) {
-    plan.chunk = (int)(((d.l + chunks - 1) / chunks + kChunkStep - 1) / kChunkStep * kChunkStep);
+  if (chunks >= (getenv("CH") ? atoi(getenv("CH")) : 5)) {
+    plan.chunk = (int)(((d.l + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
     plan.chunks = (d.l + plan.chunk - 1) / plan.chunk;
   }
   if (plan.chunks > 1) {
