@@ -26,7 +26,6 @@
 // That doubles the exponentials, so it needs more than two chunks to pay.
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include "sequence.cuh"
 
 namespace b200conv {
@@ -258,8 +257,8 @@ __device__ __forceinline__ void load_states(const T* p, float (&v)[kStates]) {
 }
 
 // kFull: states == kStates * kLanes.  kEnds: the chunk's final state from zero and its sum of delta, no output.
-template <typename T, int kStates, int kLanes, bool kFull, bool kEnds>
-__global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock) scan_kernel(const ScanArgs p) {
+template <typename T, int kStates, int kLanes, bool kFull, bool kEnds, int kBlocks>
+__global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) scan_kernel(const ScanArgs p) {
   using L = Shape<T, kStates, kLanes>;
   constexpr int kReady = 1, kDone = 3, kHelp = 5;      // barriers; the first two have one for each stage
   extern __shared__ __align__(16) unsigned char smem[];
@@ -467,11 +466,22 @@ __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock) scan_kernel
 #pragma unroll
     for (int i = 0; i < kStates; ++i)
       if (i < have) h[i] = p.ws_state[ws_row + i];
-    for (int j = 0; j < chunk; ++j) {
-      const float sum = p.ws_sum[((long long)w.seq * p.chunks + j) * p.channels + ch];
+    const float *sums = p.ws_sum + (long long)w.seq * p.chunks * p.channels + ch, *ends = p.ws_state + ws_row + ws_step;
+    constexpr int kAhead = 8;      // chunks whose loads are in flight together
+    for (int j = 0; j < chunk; j += kAhead) {
+      float sum[kAhead], from[kAhead][kStates];
 #pragma unroll
-      for (int i = 0; i < kStates; ++i)
-        if (i < have) h[i] = fmaf(decay(a2[i].x, sum), h[i], p.ws_state[ws_row + (j + 1) * ws_step + i]);
+      for (int u = 0; u < kAhead; ++u) {
+        const bool there = j + u < chunk;
+        sum[u] = there ? sums[(j + u) * (long long)p.channels] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kStates; ++i) from[u][i] = there && i < have ? ends[(j + u) * ws_step + i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < kStates; ++i)
+          if (j + u < chunk && i < have) h[i] = fmaf(decay(a2[i].x, sum[u]), h[i], from[u][i]);
     }
   } else if (p.carry) {
 #pragma unroll
@@ -710,6 +720,8 @@ int access_bytes(const void* p, const long long* stride, long long cols_a, long 
   return 0;
 }
 
+constexpr int kSms = 148;
+
 template <typename T, int kStates, int kLanes, bool kFull>
 cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
   using L = Shape<T, kStates, kLanes>;
@@ -734,10 +746,13 @@ cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
     return cudaGetLastError();
   };
   if (p.chunks > 1) {
-    cudaError_t e = run(scan_kernel<T, kStates, kLanes, kFull, true>);
+    cudaError_t e = run(scan_kernel<T, kStates, kLanes, kFull, true, 2>);
     if (e != cudaSuccess) return e;
   }
-  return run(scan_kernel<T, kStates, kLanes, kFull, false>);
+  // With a block an SM at most, the registers of two make a better schedule (8192 tokens
+  // of 4096 channels: 322 us with 206 registers, 353 with 128).
+  if (kFull && blocks * p.chunks <= kSms) return run(scan_kernel<T, kStates, kLanes, kFull, false, 1>);
+  return run(scan_kernel<T, kStates, kLanes, kFull, false, (L::kBytes > 110 * 1024 ? 1 : 2)>);
 }
 
 template <typename T>
@@ -745,7 +760,6 @@ cudaError_t scan_typed(const ScanArgs& p, const ScanPlan& plan, cudaStream_t s) 
 #define B200CONV_SCAN(S, L, F) \
   if (plan.states_per_lane == S && plan.lanes == L && (!F || p.states == S * L)) return scan_shaped<T, S, L, F>(p, s)
   B200CONV_SCAN(4, 4, true);
-  B200CONV_SCAN(2, 8, true);
   B200CONV_SCAN(2, 4, false);
   B200CONV_SCAN(4, 4, false);
   B200CONV_SCAN(4, 8, false);
@@ -795,29 +809,34 @@ cudaError_t step_typed(StepArgs p, cudaStream_t s) {
 
 }  // namespace
 
+constexpr int kLeastChunk = 64, kMostChunks = 128;
+
 // Pure in the descriptor and the device's SM count.
 ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   ScanPlan plan{};
+  // Four states a lane: with two the smem reads of b, c and delta bound the kernel
+  // (8192 tokens of 4096 channels, 16 states: 359 us on 8 lanes, 322 on 4; 16 sequences
+  // of 512 tokens 338 and 251).
   plan.states_per_lane = d.s <= 8 ? 2 : 4;
   plan.lanes = 4;
   while (plan.lanes * plan.states_per_lane < d.s) {
     if (plan.lanes < 32) plan.lanes *= 2;
     else plan.states_per_lane *= 2;
   }
-  if (d.s == 16) {
-    plan.states_per_lane = 4;
-    plan.lanes = 4;
-    if (getenv("SL")) { plan.lanes = atoi(getenv("SL")); plan.states_per_lane = 16 / plan.lanes; }
-  }
   const int channels = kScanners / plan.lanes;
   const long long per_group = d.d / d.groups;
   const long long blocks = (long long)d.n * d.groups * ((per_group + channels - 1) / channels);
   plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
   plan.chunks = 1;
-  // With chunks every token is gone over twice, so three are the fewest that can pay.
-  const long long want = blocks > 0 ? 4LL * sm_count / blocks : 0, most = (d.l + 2LL * kTile - 1) / (2 * kTile);
-  const long long chunks = want < most ? want : most;
-  if (chunks >= (getenv("CH") ? atoi(getenv("CH")) : 5)) {
+  // Cut, every token is gone over twice: it pays from four chunks on (8192 tokens of
+  // 2048 channels, 4 chunks: 242 us against 322; of 3000, 3 chunks: 355 against 338).
+  // Two blocks an SM are enough, and a chunk's start is worked out from all chunks
+  // before it, so not too many (16384 tokens of 32 channels: 27.5 us in 148 chunks,
+  // 38.6 in 256) nor too short ones.
+  const long long want = blocks > 0 ? 2LL * sm_count / blocks : 0, most = (d.l + kLeastChunk - 1LL) / kLeastChunk;
+  long long chunks = want < most ? want : most;
+  if (chunks > kMostChunks) chunks = kMostChunks;
+  if (chunks >= 4) {
     plan.chunk = (int)(((d.l + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
     plan.chunks = (d.l + plan.chunk - 1) / plan.chunk;
   }
