@@ -9,22 +9,27 @@ checks are kept short: one comparison each, the message made only on failure.
 """
 from __future__ import annotations
 
+from ctypes import byref
+
 import torch
 
 from . import binding as B
 
 _CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_F32, _I32 = torch.float32, torch.int32
+_CONTIGUOUS = torch.contiguous_format
 _stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_empty_like = torch.empty_like
 _NO_STRIDES = (0, 0, 0)
 
 
-def _refuse(t, name, shape, dtype, device, contiguous):
+def _refuse(t, name, shape, dtype, index, contiguous):
     """Raise for the first thing that is wrong with an operand."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, x on cuda:{index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
@@ -32,59 +37,62 @@ def _refuse(t, name, shape, dtype, device, contiguous):
     raise ValueError(f"{name} must be contiguous" if contiguous else f"the last dimension of {name} must be contiguous")
 
 
-def _whole(t, name, shape, dtype, device):
-    """The pointer of a contiguous operand; 0 for None."""
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype is not dtype or t.shape != shape \
-            or not t.is_contiguous():
-        _refuse(t, name, shape, dtype, device, True)
-    return t.data_ptr()
+def _whole(t, name, shape, dtype, index):
+    """The pointer of a contiguous operand."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, index, True)
 
 
-def _rows(t, name, shape, dtype, device):
+def _rows(t, name, shape, dtype, index):
     """(pointer, strides) of an operand whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype is not dtype or t.shape != shape:
-        _refuse(t, name, shape, dtype, device, False)
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] > 1:
-        _refuse(t, name, shape, dtype, device, False)
-    return t.data_ptr(), s
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape:
+            s = t.stride()
+            if s[-1] == 1 or shape[-1] == 1:
+                return t.data_ptr(), s
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, index, False)
 
 
 def _input(x, dims):
-    """(type code, device, shape, dtype) of the input that the other operands are held against."""
+    """(type code, device index, shape, dtype) of the input that the other operands are held against."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor (the library has no CPU path)")
-    code = _CODES.get(x.dtype)
+    dtype = x.dtype
+    code = _CODES.get(dtype)
     if code is None:
-        raise TypeError(f"unsupported dtype {x.dtype}")
+        raise TypeError(f"unsupported dtype {dtype}")
     shape = x.shape
     if len(shape) != dims:
         raise ValueError(f"x must have {dims} dimensions (tokens packed with offsets, or a step: [T, C]; a batch: [N, L, C])")
-    return code, x.device, shape, x.dtype
+    return code, x.get_device(), shape, dtype
 
 
-def _offsets(offsets, device):
+def _offsets(offsets, index):
     """(pointer, sequences)"""
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a tensor of n + 1 values")
-    return _whole(offsets, "offsets", offsets.shape, torch.int32, device), offsets.shape[0] - 1
+    return _whole(offsets, "offsets", offsets.shape, _I32, index), offsets.shape[0] - 1
 
 
-def _cache(state, slots, n, rows, cols, dtype, device):
+def _cache(state, slots, n, rows, cols, dtype, index):
     """(state pointer, slots pointer, slots in the cache) for n sequences."""
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError(f"state must be a tensor of shape (slots, {rows}, {cols})")
     have = state.shape[0]
-    ptr = _whole(state, "state", (have, rows, cols), dtype, device)
+    ptr = _whole(state, "state", (have, rows, cols), dtype, index)
     if slots is None:
         if have < n:
             raise ValueError(f"state has {have} slots for {n} sequences")
         return ptr, 0, have
     if have < 1:
         raise ValueError("state has no slots")
-    return ptr, _whole(slots, "slots", (n,), torch.int32, device), have
+    return ptr, _whole(slots, "slots", (n,), _I32, index), have
 
 
 def _need_state(state, slots, carry):
@@ -105,9 +113,8 @@ def _activation(name):
     return code
 
 
-def _enqueue(call, device, *args):
-    """call(*args, stream) on torch's current stream of `device`, that device current."""
-    index = device.index
+def _enqueue(call, index, *args):
+    """call(*args, stream) on torch's current stream of device `index`, that device current."""
     if index == _current_device():
         status = call(*args, _stream(index))
     else:
@@ -124,20 +131,20 @@ def conv1d_causal(x, w, bias=None, activation=None, offsets=None, state=None, sl
     sequence are zero, or with carry its slot of state [slots, K-1, C]; the last K-1
     tokens are left in state where one is given.  x may be a slice of wider rows."""
     packed = offsets is not None
-    code, device, shape, dtype = _input(x, 2 if packed else 3)
+    code, index, shape, dtype = _input(x, 2 if packed else 3)
     _need_state(state, slots, carry)
-    op, n = _offsets(offsets, device) if packed else (0, shape[0])
+    op, n = _offsets(offsets, index) if packed else (0, shape[0])
     c, k = shape[-1], _filter(w)
-    xp, xs = _rows(x, "x", shape, dtype, device)
-    wp = _whole(w, "w", (c, k), dtype, device)
-    bp = _whole(bias, "bias", (c,), dtype, device)
-    sp, ip, have = (0, 0, 0) if state is None else _cache(state, slots, n, k - 1, c, dtype, device)
+    xp, xs = _rows(x, "x", shape, dtype, index)
+    wp = _whole(w, "w", (c, k), dtype, index)
+    bp = 0 if bias is None else _whole(bias, "bias", (c,), dtype, index)
+    sp, ip, have = (0, 0, 0) if state is None else _cache(state, slots, n, k - 1, c, dtype, index)
     if out is None:
-        out = x.new_empty(shape)
-    yp, ys = _rows(out, "out", shape, dtype, device)
+        out = _empty_like(x, memory_format=_CONTIGUOUS)
+    yp, ys = _rows(out, "out", shape, dtype, index)
     desc = B.CausalConvDesc(n, shape[-2], c, k, _activation(activation), 1 if carry else 0, have,
                             0 if packed else xs[0], xs[-2], 0 if packed else ys[0], ys[-2])
-    _enqueue(B.conv1d_causal_forward, device, xp, wp, bp, op, sp, ip, yp, desc, code)
+    _enqueue(B._conv1d_causal_forward, index, xp, wp, bp, op, sp, ip, yp, byref(desc), code)
     return out
 
 
@@ -145,23 +152,23 @@ def conv1d_causal_step(x, w, state, bias=None, activation=None, slots=None, out=
     """conv1d_causal for one new token of each of N sequences: x [N, C], the window of
     sequence i in slot i, or slots[i], of state [slots, K-1, C], shifted in place.  A
     sequence whose slot is outside the cache (-1) is left out, its row of out too."""
-    code, device, shape, dtype = _input(x, 2)
+    code, index, shape, dtype = _input(x, 2)
     (n, c), k = shape, _filter(w)
-    xp, xs = _rows(x, "x", shape, dtype, device)
-    wp = _whole(w, "w", (c, k), dtype, device)
-    bp = _whole(bias, "bias", (c,), dtype, device)
-    sp, ip, have = _cache(state, slots, n, k - 1, c, dtype, device)
+    xp, xs = _rows(x, "x", shape, dtype, index)
+    wp = _whole(w, "w", (c, k), dtype, index)
+    bp = 0 if bias is None else _whole(bias, "bias", (c,), dtype, index)
+    sp, ip, have = _cache(state, slots, n, k - 1, c, dtype, index)
     if out is None:
-        out = x.new_empty(shape)
-    yp, ys = _rows(out, "out", shape, dtype, device)
+        out = _empty_like(x, memory_format=_CONTIGUOUS)
+    yp, ys = _rows(out, "out", shape, dtype, index)
     desc = B.CausalConvDesc(n, 1, c, k, _activation(activation), 1, have, xs[0], 0, ys[0], 0)
-    _enqueue(B.conv1d_causal_step_forward, device, xp, wp, bp, sp, ip, yp, desc, code)
+    _enqueue(B._conv1d_causal_step_forward, index, xp, wp, bp, sp, ip, yp, byref(desc), code)
     return out
 
 
-def _states(t, name, lead, g, s, dtype, device):
+def _states(t, name, lead, g, s, dtype, index):
     """(pointer, strides) of b or c, [..., G, S] with the last two dimensions contiguous."""
-    p, st = _rows(t, name, (*lead, g, s), dtype, device)
+    p, st = _rows(t, name, (*lead, g, s), dtype, index)
     if g > 1 and st[-2] != s:
         raise ValueError(f"the last two dimensions of {name} must be contiguous")
     return p, st
@@ -187,28 +194,28 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=False,
     in fp32.  h starts from zero, or with carry from state [slots, D, S] (fp32), and is
     left there where one is given.  x, dt, z, b, c may be slices of wider rows."""
     packed = offsets is not None
-    code, device, shape, dtype = _input(x, 2 if packed else 3)
+    code, index, shape, dtype = _input(x, 2 if packed else 3)
     _need_state(state, slots, carry)
-    op, n = _offsets(offsets, device) if packed else (0, shape[0])
+    op, n = _offsets(offsets, index) if packed else (0, shape[0])
     lead, dim = shape[:-1], shape[-1]
     g, s = _groups(b, len(shape), dim)
-    xp, xs = _rows(x, "x", shape, dtype, device)
-    tp, ts = _rows(dt, "dt", shape, dtype, device)
-    bp, bs = _states(b, "b", lead, g, s, dtype, device)
-    cp, cs = _states(c, "c", lead, g, s, dtype, device)
-    zp, zs = (0, _NO_STRIDES) if z is None else _rows(z, "z", shape, dtype, device)
-    ap = _whole(a, "a", (dim, s), torch.float32, device)
-    dp = _whole(d, "d", (dim,), torch.float32, device)
-    up = _whole(dt_bias, "dt_bias", (dim,), torch.float32, device)
-    sp, ip, have = (0, 0, 0) if state is None else _cache(state, slots, n, dim, s, torch.float32, device)
+    xp, xs = _rows(x, "x", shape, dtype, index)
+    tp, ts = _rows(dt, "dt", shape, dtype, index)
+    bp, bs = _states(b, "b", lead, g, s, dtype, index)
+    cp, cs = _states(c, "c", lead, g, s, dtype, index)
+    zp, zs = (0, _NO_STRIDES) if z is None else _rows(z, "z", shape, dtype, index)
+    ap = _whole(a, "a", (dim, s), _F32, index)
+    dp = 0 if d is None else _whole(d, "d", (dim,), _F32, index)
+    up = 0 if dt_bias is None else _whole(dt_bias, "dt_bias", (dim,), _F32, index)
+    sp, ip, have = (0, 0, 0) if state is None else _cache(state, slots, n, dim, s, _F32, index)
     if out is None:
-        out = x.new_empty(shape)
-    yp, ys = _rows(out, "out", shape, dtype, device)
+        out = _empty_like(x, memory_format=_CONTIGUOUS)
+    yp, ys = _rows(out, "out", shape, dtype, index)
     t = len(shape) - 2                                  # the token dimension; a packed call has no batch before it
     batch = (lambda st: 0) if packed else (lambda st: st[0])
     desc = B.ScanDesc(n, shape[t], dim, s, g, 1 if softplus else 0, 1 if carry else 0, have, batch(xs), xs[t], batch(ts),
                       ts[t], batch(zs), zs[t], batch(bs), bs[t], batch(cs), cs[t], batch(ys), ys[t])
-    need = B.selective_scan_workspace_size(desc, code, device.index)
+    need = B._selective_scan_workspace_size(byref(desc), code, index)
     if workspace is not None:
         B._check_workspace(workspace, need, x)
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -218,7 +225,7 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=False,
     else:
         wp = wn = 0
     tensors = B.ScanTensors(xp, tp, bp, cp, zp, ap, dp, up, op, ip, sp, yp)
-    _enqueue(B.selective_scan_forward, device, tensors, desc, code, wp, wn)
+    _enqueue(B._selective_scan_forward, index, byref(tensors), byref(desc), code, wp, wn)
     return out
 
 
@@ -227,23 +234,23 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, sof
     [N, G, S], the state of sequence i in slot i, or slots[i], of state [slots, D, S]
     (fp32), advanced in place.  A sequence whose slot is outside the cache (-1) is left
     out, its row of out too."""
-    code, device, shape, dtype = _input(x, 2)
+    code, index, shape, dtype = _input(x, 2)
     n, dim = shape
     g, s = _groups(b, 2, dim)
-    xp, xs = _rows(x, "x", shape, dtype, device)
-    tp, ts = _rows(dt, "dt", shape, dtype, device)
-    bp, bs = _states(b, "b", (n,), g, s, dtype, device)
-    cp, cs = _states(c, "c", (n,), g, s, dtype, device)
-    zp, zs = (0, _NO_STRIDES) if z is None else _rows(z, "z", shape, dtype, device)
-    ap = _whole(a, "a", (dim, s), torch.float32, device)
-    dp = _whole(d, "d", (dim,), torch.float32, device)
-    up = _whole(dt_bias, "dt_bias", (dim,), torch.float32, device)
-    sp, ip, have = _cache(state, slots, n, dim, s, torch.float32, device)
+    xp, xs = _rows(x, "x", shape, dtype, index)
+    tp, ts = _rows(dt, "dt", shape, dtype, index)
+    bp, bs = _states(b, "b", (n,), g, s, dtype, index)
+    cp, cs = _states(c, "c", (n,), g, s, dtype, index)
+    zp, zs = (0, _NO_STRIDES) if z is None else _rows(z, "z", shape, dtype, index)
+    ap = _whole(a, "a", (dim, s), _F32, index)
+    dp = 0 if d is None else _whole(d, "d", (dim,), _F32, index)
+    up = 0 if dt_bias is None else _whole(dt_bias, "dt_bias", (dim,), _F32, index)
+    sp, ip, have = _cache(state, slots, n, dim, s, _F32, index)
     if out is None:
-        out = x.new_empty(shape)
-    yp, ys = _rows(out, "out", shape, dtype, device)
+        out = _empty_like(x, memory_format=_CONTIGUOUS)
+    yp, ys = _rows(out, "out", shape, dtype, index)
     desc = B.ScanDesc(n, 1, dim, s, g, 1 if softplus else 0, 1, have, xs[0], 0, ts[0], 0, zs[0], 0, bs[0], 0, cs[0], 0,
                       ys[0], 0)
     tensors = B.ScanTensors(xp, tp, bp, cp, zp, ap, dp, up, 0, ip, sp, yp)
-    _enqueue(B.selective_scan_step_forward, device, tensors, desc, code)
+    _enqueue(B._selective_scan_step_forward, index, byref(tensors), byref(desc), code)
     return out
