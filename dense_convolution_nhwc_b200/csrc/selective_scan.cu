@@ -613,15 +613,15 @@ struct StepArgs {
 // (delta and the gate), and that many loads are in flight.  One channel at a time
 // took 260 instructions for four states, mostly addresses and the softplus.
 template <typename T, int kLanes, int kMine, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
+__global__ void __launch_bounds__(kThreads, 6) scan_step_kernel(const StepArgs p) {
   constexpr int kAcross = 32 / kLanes, kSub = kLanes / kMine;   // channels side by side; lanes that hold one channel's token
   const int seq = blockIdx.z * gridDim.y + blockIdx.y;
   if (seq >= p.n) return;
-  const int slot = slot_of(p.slots, seq, p.state_slots);
-  if (slot < 0) return;
   const int lane = threadIdx.x % kLanes;
   const int first = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kAcross * kMine + threadIdx.x % 32 / kLanes;
   const int mine = first + lane / kSub * kAcross;
+  // Only the state hangs on the slot: everything else is asked for before the slot is looked at.
+  const int slot = slot_of(p.slots, seq, p.state_slots);
   float xv = 0.0f, delta = 0.0f, skip = 0.0f, gate = 1.0f;
   if (mine < p.channels) {
     xv = ld_f32(static_cast<const T*>(p.x) + seq * p.x_s + mine);
@@ -634,29 +634,14 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
   const int group = p.groups > 1 ? min(first, p.channels - 1) / (p.channels / p.groups) : 0;
   const T* b = static_cast<const T*>(p.b) + seq * p.b_s + group * p.states;
   const T* c = static_cast<const T*>(p.c) + seq * p.c_s + group * p.states;
-  float* state = p.state + (long long)slot * p.channels * p.states;
+  float* state = p.state + (long long)max(slot, 0) * p.channels * p.states;
   float de2[kMine], dx[kMine], y[kMine];
 #pragma unroll
   for (int q = 0; q < kMine; ++q) y[q] = 0.0f;
-  bool ready = false;
-  for (int s = lane * 4; s < (p.states + 3) / 4 * 4 || !ready; s += kLanes * 4) {
+  // the lanes past the states take part in the first turn's shuffles
+  for (int s = lane * 4, turn = 0; turn == 0 || s < p.states; s += kLanes * 4, ++turn) {
     const int have = min(max(p.states - s, 0), 4);
     float av[kMine][4], h[kMine][4], bv[4], cv[4];
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int ch = min(first + q * kAcross, p.channels - 1);
-      const float *hp = state + (long long)ch * p.states + s, *ap = p.a + (long long)ch * p.states + s;
-      if (VEC && have == 4) {
-        load_f32<float, 4, true>(hp, h[q]);
-        load_f32<float, 4, true>(ap, av[q]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[q][i] = i < have ? hp[i] : 0.0f;
-          av[q][i] = i < have ? __ldg(ap + i) : 0.0f;
-        }
-      }
-    }
     if (p.bc_vec && have == 4) {
       load_f32<T, 4, true>(b + s, bv);
       load_f32<T, 4, true>(c + s, cv);
@@ -667,8 +652,28 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const StepArgs p) {
         cv[i] = i < have ? ld_f32(c + s + i) : 0.0f;
       }
     }
-    if (!ready) {                 // behind the loads' issue: they do not wait for it
-      ready = true;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const float* ap = p.a + (long long)min(first + q * kAcross, p.channels - 1) * p.states + s;
+      if (VEC && have == 4) {
+        load_f32<float, 4, true>(ap, av[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[q][i] = i < have ? __ldg(ap + i) : 0.0f;
+      }
+    }
+    if (slot < 0) return;         // the whole block's
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const float* hp = state + (long long)min(first + q * kAcross, p.channels - 1) * p.states + s;
+      if (VEC && have == 4) {
+        load_f32<float, 4, true>(hp, h[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[q][i] = i < have ? hp[i] : 0.0f;
+      }
+    }
+    if (turn == 0) {
       if (p.softplus) delta = softplus(delta);
       const float mine_de2 = delta * kLog2e, mine_dx = delta * xv;
 #pragma unroll
