@@ -95,10 +95,20 @@ struct Stager {
     } else if (bytes == 4) {
       by<4>(dst, rows);
     } else {
-#pragma unroll 8
-      for (int i = me; i < rows * kCols; i += kN) {
-        const int r = i / kCols, q = i % kCols;
-        if (q < cols) dst[r * kCols + q] = src[r * stride + q];
+      // several loads, then their stores: one after the other each would wait for the last
+      constexpr int kAll = (kRows * kCols + kN - 1) / kN, kBatch = kAll < 8 ? kAll : 8;
+      for (int i0 = me; i0 < rows * kCols; i0 += kBatch * kN) {
+        T v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kN, r = i / kCols, q = i % kCols;
+          if (r < rows && q < cols) v[k] = src[r * stride + q];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kN, r = i / kCols, q = i % kCols;
+          if (r < rows && q < cols) dst[i] = v[k];
+        }
       }
     }
     src += kRows * stride;
@@ -362,9 +372,9 @@ __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) sc
       for (int i = me; i < 2 * L::kRing * kTile * pad; i += L::kHelpers)
         b_at(0)[i / pad * L::kWide + p.states + i % pad] = Store<T>::from_f32(0.0f);
     }
+    load(0);                // first: where b and c are copied element by element, the fetches wait for them
 #pragma unroll
     for (int i = 0; i < L::kRing - 1; ++i) fetch(i);
-    load(0);
     for (int tile = 0; tile < tiles; ++tile) {
       const int stage = tile & 1;
       now_x = next_x;
