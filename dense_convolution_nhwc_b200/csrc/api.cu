@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -75,19 +76,16 @@ conv_status_t device_state(int dev, DeviceState** out) {
   return CONV_OK;
 }
 
-// The SM count alone, without the error word's lookup (the sequence operators have no waits to report).
+// The SM count alone.  No error word is looked up or cleared for it, so that a
+// sequence operator may be a process's first call inside a stream capture.
 conv_status_t device_sm_count(int dev, int* sms) {
-  if (dev >= 0 && dev < kMaxDevices) {
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    if (g_dev[dev].ready) {
-      *sms = g_dev[dev].props.sm_count;
-      return CONV_OK;
-    }
-  }
-  DeviceState* d = nullptr;
-  conv_status_t st = device_state(dev, &d);
-  if (st == CONV_OK) *sms = d->props.sm_count;
-  return st;
+  static std::atomic<int> known[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return CONV_ERR_INVALID;
+  *sms = known[dev].load(std::memory_order_relaxed);
+  if (*sms > 0) return CONV_OK;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms <= 0) return CONV_ERR_CUDA;
+  known[dev].store(*sms, std::memory_order_relaxed);
+  return CONV_OK;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1058,7 +1056,7 @@ conv_status_t run3d_winograd(const void* in, const void* w, void* out, const Geo
 
 namespace {
 
-constexpr int kMaxTokens = 1 << 30;
+constexpr int kMaxTokens = 1 << 30, kMaxChannels = 1 << 22;
 
 // The memory between a tensor's first and last element.
 struct Span {
@@ -1082,7 +1080,7 @@ bool valid_strides(const long long* s, long long n, long long l, long long cols,
 
 conv_status_t check_causal(const conv1d_causal_desc_t* d, conv_dtype_t dt, bool state, bool slots) {
   if (!d || !valid_dtype(dt)) return CONV_ERR_INVALID;
-  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->c <= 0 || d->k < 2 || d->k > 8) return CONV_ERR_INVALID;
+  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->c <= 0 || d->c > kMaxChannels || d->k < 2 || d->k > 8) return CONV_ERR_INVALID;
   if (d->activation != CONV_ACT_NONE && d->activation != CONV_ACT_SILU) return CONV_ERR_INVALID;
   if (!state && (d->carry || slots)) return CONV_ERR_INVALID;
   if (state && d->state_slots < (slots ? 1 : d->n)) return CONV_ERR_INVALID;
@@ -1115,7 +1113,7 @@ conv_status_t check_causal_tensors(const void* x, const void* w, const void* bia
 
 conv_status_t check_scan(const selective_scan_desc_t* d, conv_dtype_t dt) {
   if (!d || !valid_dtype(dt)) return CONV_ERR_INVALID;
-  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->d <= 0 || d->s <= 0 || d->s > 256) return CONV_ERR_INVALID;
+  if (d->n < 0 || d->l < 0 || d->l > kMaxTokens || d->d <= 0 || d->d > kMaxChannels || d->s <= 0 || d->s > 256) return CONV_ERR_INVALID;
   if (d->groups <= 0 || d->d % d->groups != 0) return CONV_ERR_INVALID;
   return CONV_OK;
 }

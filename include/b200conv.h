@@ -240,14 +240,14 @@ B200CONV_API conv_status_t conv1d_forward(const void *in, const void *w, void *o
  *  - State lives in a cache of state_slots slots owned by the caller and is
  *    updated in place.  Sequence i uses slot slots[i] (int32 on the device), or
  *    slot i when slots is NULL.  A sequence whose slot is outside the cache (-1,
- *    say) is left out: nothing of it is read or written.  The slots of one call
+ *    say) is left out: nothing of it is written.  The slots of one call
  *    must differ from each other; where two are equal, what that slot holds
  *    afterwards is unspecified.
  *  - carry != 0: each sequence continues from its slot.  carry == 0: each
  *    starts from zero (whatever its slot holds) and leaves its state there.  For
  *    a mix, clear the slots of the new sequences and carry.  state may be NULL
  *    when carry is 0 and slots is NULL: nothing is kept.  A step always carries.
- *  - At most 2^30 tokens a sequence or packed call.  out and state must not
+ *  - At most 2^30 tokens a sequence or packed call and 2^22 channels.  out and state must not
  *    overlap each other or any input (CONV_ERR_INVALID); the spans between a
  *    tensor's first and last element are compared.
  * Inputs and out are of `dtype` (weights and bias of the convolution too);

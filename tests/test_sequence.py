@@ -33,7 +33,7 @@ X, W, BIAS, STATE, OUT, SLOTS, OFFSETS = (0x100000 * i for i in range(1, 8))
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(n=-1), 1), (dict(l=-1), 1), (dict(l=2 ** 30 + 1), 1), (dict(c=0), 1), (dict(k=1), 1), (dict(k=9), 1),
+    (dict(n=-1), 1), (dict(l=-1), 1), (dict(l=2 ** 30 + 1), 1), (dict(c=0), 1), (dict(c=2 ** 22 + 1), 1), (dict(k=1), 1), (dict(k=9), 1),
     (dict(activation=2), 1), (dict(state_slots=1), 1), (dict(x_stride=(-1, 8)), 1), (dict(out_stride=(40, 7)), 1),
     (dict(out_stride=(39, 8)), 1), (dict(n=0), 0),
 ])
@@ -77,7 +77,7 @@ def scan_tensors(**over):
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(n=-1), 1), (dict(l=-1), 1), (dict(l=2 ** 30 + 1), 1), (dict(d=0), 1), (dict(s=0), 1), (dict(s=257), 1),
+    (dict(n=-1), 1), (dict(l=-1), 1), (dict(l=2 ** 30 + 1), 1), (dict(d=0), 1), (dict(d=2 ** 22 + 2), 1), (dict(s=0), 1), (dict(s=257), 1),
     (dict(groups=0), 1), (dict(groups=3), 1), (dict(state_slots=1), 1), (dict(b_stride=(160, -1)), 1),
     (dict(out_stride=(40, 7)), 1), (dict(n=0), 0),
 ])
@@ -684,3 +684,128 @@ def test_empty_calls():
     empty = torch.empty(0, 8, device="cuda")
     off = torch.zeros(1, dtype=torch.int32, device="cuda")
     assert dc.conv1d_causal(empty, w, offsets=off).shape == (0, 8)
+
+
+@gpu
+def test_many_short_sequences():
+    """Thousands of packed sequences of none to three tokens, and slots in any order."""
+    torch.manual_seed(23)
+    lens = torch.randint(0, 4, (2500,)).tolist()
+    order = torch.randperm(2502)[:2500].tolist()
+    check_conv(torch.float16, 4, 16, lens, True, True, True, True, tail=5, slots=order)
+    check_scan(torch.bfloat16, 9, 6, 1, lens, True, True, tail=5, slots=order)
+
+
+@gpu
+@pytest.mark.parametrize("lens,slots", [([300, 0, 5, 270], [5, -1, 0, 2]), ([500, 40], [7, 1])])
+def test_cut_scan_with_slots(lens, slots):
+    assert B.selective_scan_workspace_size(B.ScanDesc(len(lens), sum(lens) + 2, 12, 16, 2), 0, 0) > 0
+    for carry in (False, True):
+        check_scan(torch.float16, 12, 16, 2, lens, True, carry, tail=2, slots=slots, gap=3)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scan_wide_states_over_many_tiles(dtype):
+    """More tiles than the rings of b and c hold, at the widest states."""
+    for s in (100, 200, 256):
+        check_scan(TYPES[dtype], 70, s, 1, [200, 131], True, True, seed=s)
+
+
+@gpu
+def test_broadcast_inputs_and_strided_outputs():
+    """One x for every sequence (batch stride 0), outputs into a slice of wider rows."""
+    normal = draws(25)
+    torch.manual_seed(25)
+    x = normal(1, 50, 24, dtype=torch.bfloat16).expand(3, 50, 24)
+    w = normal(24, 4, dtype=torch.bfloat16)
+    wide = torch.full((3, 50, 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = dc.conv1d_causal(x, w, out=wide[..., 8:32])
+    assert torch.equal(got, dc.conv1d_causal(x.contiguous(), w))
+    assert (wide[..., :8] == 7).all() and (wide[..., 32:] == 7).all()
+    t = scan_inputs(normal, (3, 50), 24, 16, 1, torch.bfloat16)
+    want = dc.selective_scan(**dict(t, x=x.contiguous()), softplus=True)
+    wide.fill_(7.0)
+    got = dc.selective_scan(**dict(t, x=x), softplus=True, out=wide[..., 3:27])
+    assert torch.equal(got, want) and (wide[..., :3] == 7).all() and (wide[..., 27:] == 7).all()
+
+
+@gpu
+def test_two_calls_at_once():
+    """Cut scans, each with a workspace of its own, side by side on two streams."""
+    normal = draws(27)
+    torch.manual_seed(27)
+    inputs = [scan_inputs(normal, (1, 4000), 32, 16, 1, torch.float32) for _ in range(2)]
+    want = [dc.selective_scan(**t, softplus=True) for t in inputs]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for t, s in zip(inputs, streams):
+            with torch.cuda.stream(s):
+                got.append(dc.selective_scan(**t, softplus=True))
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, v) for g, v in zip(got, want))
+
+
+@gpu
+def test_infinite_input_with_states_that_do_not_fill_the_lanes():
+    """An infinite x gives the states that exist infinities and the others nothing: the
+    outputs are infinite, not NaN, where b and c agree in sign; prompt and step alike."""
+    normal = draws(29)
+    torch.manual_seed(29)
+    for s in (3, 5, 11, 20, 70):
+        t = scan_inputs(normal, (2, 20), 8, s, 1, torch.float32, gate=False)
+        t["b"], t["c"] = t["b"].abs() + 0.1, t["c"].abs() + 0.1
+        t["x"] = t["x"].abs()
+        t["x"][0, 7, 2] = float("inf")
+        got = dc.selective_scan(**t, softplus=True)
+        assert (got[0, 7:, 2] == float("inf")).all() and got[0, :7].isfinite().all() and got[1].isfinite().all()
+        state = torch.zeros(2, 8, s, device="cuda")
+        one = {k: v if k in ("a", "d", "dt_bias") or v is None else v[:, 7] for k, v in t.items()}
+        step = dc.selective_scan_step(**one, state=state, softplus=True)
+        assert step[0, 2] == float("inf") and state[0, 2].eq(float("inf")).all() and step[1].isfinite().all()
+
+
+@gpu
+def test_the_same_slot_twice_stays_inside():
+    """What such a slot holds is unspecified; nothing else changes."""
+    normal = draws(31)
+    torch.manual_seed(31)
+    t = scan_inputs(normal, (3,), 16, 16, 1, torch.float32)
+    guard = Guarded(5 * 16 * 16 * 4, "cuda")
+    state = guard.tensor((5, 16, 16), torch.float32)
+    state.copy_(normal(5, 16, 16))
+    before = state.clone()
+    dc.selective_scan_step(**t, state=state, softplus=True, slots=torch.tensor([1, 1, 4], dtype=torch.int32, device="cuda"))
+    window = normal(5, 3, 16)
+    kept = window.clone()
+    dc.conv1d_causal_step(t["x"], normal(16, 4), window, slots=torch.tensor([2, 2, 0], dtype=torch.int32, device="cuda"))
+    guard.assert_intact("state")
+    assert torch.equal(state[[0, 2, 3]], before[[0, 2, 3]]) and torch.equal(window[[1, 3, 4]], kept[[1, 3, 4]])
+
+
+@gpu
+def test_log_line(capfd, monkeypatch):
+    """B200CONV_LOG=1 prints one line a call, like the convolutions."""
+    monkeypatch.setenv("B200CONV_LOG", "1")
+    normal = draws(33)
+    torch.manual_seed(33)
+    t = scan_inputs(normal, (1, 700), 16, 16, 1, torch.bfloat16)
+    dc.selective_scan(**t, softplus=True)
+    dc.conv1d_causal(t["x"], normal(16, 4, dtype=torch.bfloat16), activation="silu")
+    lines = [line for line in capfd.readouterr().err.splitlines() if line.startswith("b200conv:")]
+    assert len(lines) == 2 and "selective_scan n1 l700 d16 s16 g1 bf16" in lines[0] and "chunks=" in lines[0]
+    assert "conv1d_causal n1 l700 c16 k4 bf16" in lines[1]
+
+
+@gpu
+def test_kernels_are_timed_by_name():
+    normal = draws(35)
+    torch.manual_seed(35)
+    t = scan_inputs(normal, (1, 30), 16, 16, 1, torch.bfloat16)
+    assert B.conv_profile_begin() == 0
+    dc.selective_scan(**t, softplus=True)
+    dc.conv1d_causal(t["x"], normal(16, 4, dtype=torch.bfloat16))
+    times = B.profile_end()
+    assert times["selective_scan"][0] == 1 and times["causal_conv"][0] == 1
