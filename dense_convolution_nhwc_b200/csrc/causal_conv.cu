@@ -168,6 +168,7 @@ struct Walk {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
           load_f32<T, V, true>(reinterpret_cast<const T*>(mine + (slot_in_ring + u) * step_of), now[u]);
+        asm volatile("" ::: "memory");       // read before the next copy into the same place is issued
         fetch(slot_in_ring, to - at - kAhead);
         slot_in_ring = slot_in_ring + kBatch == kAhead ? 0 : slot_in_ring + kBatch;
 #pragma unroll

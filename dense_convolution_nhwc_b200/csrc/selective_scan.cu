@@ -9,21 +9,33 @@
 //
 // all in fp32 whatever the io type, out rounded once.
 //
-// Prompts are bound by the exponentials: one a (token, channel, state), 16 a
-// clock and SM in the special-function units, where reading and writing a
-// token's four io values costs a quarter of that.  kLanes lanes share a channel
-// with kStates states each in registers; a block of 128 threads holds 128 / kLanes
-// channels and walks the sequence in tiles of 64 tokens staged in shared
-// memory, the next tile in flight by cp.async.  Per tile the delta and
-// delta * x of each (token, channel) are computed once, spread over the channel's
-// lanes, and the sums over states of kLanes (at least 8) tokens are reduced
-// together, so that each lane ends with the sums of its own tokens.
+// Prompts.  The floor is the exponentials: one a (token, channel, state) and four
+// more a (token, channel) for softplus and gate, 16 a clock and SM in the
+// special-function units.  8192 tokens of 4096 channels and 16 states are 671 million,
+// 150 us; their 270 MB of io would take 41 us.  What the kernel spends its time on
+// besides is issue slots and shared-memory reads, so both are kept down:
+//  * kLanes lanes share a channel, kStates states each in registers; four states a
+//    lane (of 16) read b, c and delta a quarter as often as one would.
+//  * Two tokens' arguments, additions and sums are one packed instruction each; only
+//    the h chain itself is sequential.  A tile of 32 tokens is one straight piece of
+//    code (in pieces of 16: 334 us, of 8: 366 us, against 309 us).
+//  * The sums over a channel's lanes are taken for 8 tokens together, so that each lane
+//    ends with its own tokens' sums (24 instructions for 8 tokens, not 6 for each).
+//  * The rest is done by other warps beside the scanning ones: a helping thread owns one
+//    token of a tile and eight channels, loads x, dt and z straight into registers a
+//    tile ahead, works out delta and delta x, and finishes the tile before while the
+//    scanners are at this one.  Done by the scanning warps themselves between their
+//    tiles, the call took 393 us.  b becomes fp32 pairs on the way, c stays as it comes:
+//    both in fp32 the shared-memory reads bound the kernel, neither the conversions do.
+// 8192 tokens of 4096 bf16 channels: 309 us (49 % of the exponentials' rate; one block an
+// SM, bound by the latency of one scanning warp a scheduler: 72 clocks a token).  16
+// sequences of 512 tokens: 239 us (63 %).
 //
-// A call with too few channels to fill the device cuts the sequences into
-// chunks: scan_chunk_kernel leaves each chunk's final state from zero and its
-// sum of delta in the workspace, and every chunk of scan_kernel folds those
-// before it into its first state (the decay over a chunk is exp(a sum delta)).
-// That doubles the exponentials, so it needs more than two chunks to pay.
+// A call with too few channels to fill the device cuts the sequences into chunks: a
+// first launch leaves each chunk's final state from zero and its sum of delta in the
+// workspace, and every chunk of the second folds those before it into its first state
+// (the decay over a chunk is exp(a sum delta)).  That doubles the exponentials.  16384
+// tokens of 96 fp32 channels: 35 us.
 #include <cuda_runtime.h>
 
 #include "sequence.cuh"
@@ -151,6 +163,7 @@ __device__ __forceinline__ void bar_arrive(int stage) {
   asm volatile("bar.arrive %0, %1;" ::"r"(kId + stage), "n"(kN) : "memory");
 }
 
+constexpr int kSms = 148;
 constexpr int kTile = 32;   // tokens a tile, one to a lane of the helping warps
 
 template <typename T, int kStates, int kLanes>
@@ -613,6 +626,8 @@ __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) sc
 
 // ------------------------------ single tokens ----------------------------------
 
+constexpr int kWalkBlocks = 5;      // of a walking step, an SM
+
 struct StepArgs {
   const void *x, *dt, *b, *c, *z;
   const float *a, *d, *dt_bias;
@@ -629,7 +644,8 @@ struct StepArgs {
 // access with VEC), and go through kMine channels together: b and c are loaded and
 // converted once for them, each lane prepares and finishes one channel's token
 // (delta and the gate), and that many loads are in flight.  One channel at a time
-// took 260 instructions for four states, mostly addresses and the softplus.
+// took 260 instructions for four states, mostly addresses and the softplus (192
+// sequences of 4096 channels, 16 states: 38 us, with four channels 26 us = 4.1 TB/s).
 template <typename T, int kLanes, int kMine, bool VEC>
 __global__ void __launch_bounds__(kThreads, 6) scan_step_kernel(const StepArgs p) {
   constexpr int kAcross = 32 / kLanes, kSub = kLanes / kMine;   // channels side by side; lanes that hold one channel's token
@@ -730,6 +746,86 @@ __global__ void __launch_bounds__(kThreads, 6) scan_step_kernel(const StepArgs p
   }
 }
 
+// The same where a block goes through several sequences (all accesses of four states,
+// at most 4 kLanes of them): a is read once, and the next sequence's state, token, b
+// and c are on their way while the present one's are worked on, its slot two ahead.
+// 192 sequences of 4096 channels, 16 states, their slots scattered: 20.2 us = 5.3 TB/s, 81 %
+// of the copy rate.
+template <typename T, int kLanes, int kMine>
+__global__ void __launch_bounds__(kThreads, kWalkBlocks) scan_step_walk_kernel(const StepArgs p) {
+  constexpr int kAcross = 32 / kLanes, kSub = kLanes / kMine;
+  const int lane = threadIdx.x % kLanes, s = lane * 4;
+  const bool have = s < p.states;
+  const int first = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kAcross * kMine + threadIdx.x % 32 / kLanes;
+  const int mine = first + lane / kSub * kAcross, mine_in = min(mine, p.channels - 1);
+  const int group = p.groups > 1 ? min(first, p.channels - 1) / (p.channels / p.groups) : 0;
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + mine_in) : 0.0f, skip = p.d ? __ldg(p.d + mine_in) : 0.0f;
+  float av[kMine][4];
+  int at[kMine];               // of the lane's states in a slot
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    at[q] = min(first + q * kAcross, p.channels - 1) * p.states + s;
+    if (have) load_f32<float, 4, true>(p.a + at[q], av[q]);
+  }
+  struct Next {
+    T x, dt, z;
+    Held<T, 4> b, c;
+    float h[kMine][4];
+  } next;
+  auto load = [&](int seq, int slot) {
+    if (slot < 0) return;
+    next.x = static_cast<const T*>(p.x)[seq * p.x_s + mine_in];
+    next.dt = static_cast<const T*>(p.dt)[seq * p.dt_s + mine_in];
+    if (p.z) next.z = static_cast<const T*>(p.z)[seq * p.z_s + mine_in];
+    if (have) {
+      next.b.load(static_cast<const T*>(p.b) + seq * p.b_s + group * p.states + s, true, 4);
+      next.c.load(static_cast<const T*>(p.c) + seq * p.c_s + group * p.states + s, true, 4);
+      const float* state = p.state + (long long)slot * p.channels * p.states;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) load_f32<float, 4, true>(state + at[q], next.h[q]);
+    }
+  };
+  auto slot_at = [&](long long seq) { return seq < p.n ? slot_of(p.slots, (int)seq, p.state_slots) : -1; };
+  const int step = gridDim.y;
+  int slot = slot_at(blockIdx.y), slot_next = slot_at((long long)blockIdx.y + step);
+  load(blockIdx.y, slot);
+  for (long long seq = blockIdx.y; seq < p.n; seq += step) {
+    Next now = next;
+    const int slot_now = slot;
+    slot = slot_next;
+    slot_next = slot_at(seq + 2LL * step);
+    if (seq + step < p.n) load((int)(seq + step), slot);
+    if (slot_now < 0) continue;
+    const float xv = Store<T>::to_f32(now.x);
+    float delta = Store<T>::to_f32(now.dt) + bias;
+    if (p.softplus) delta = softplus(delta);
+    const float mine_de2 = delta * kLog2e, mine_dx = delta * xv;
+    float y[kMine];
+    float* state = p.state + (long long)slot_now * p.channels * p.states;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const float de2 = __shfl_sync(0xffffffffu, mine_de2, q * kSub, kLanes);
+      const float dx = __shfl_sync(0xffffffffu, mine_dx, q * kSub, kLanes);
+      y[q] = 0.0f;
+      if (have) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          now.h[q][i] = fmaf(decay(av[q][i], de2), now.h[q][i], dx * now.b.at(i));
+          y[q] = fmaf(now.c.at(i), now.h[q][i], y[q]);
+        }
+        if (first + q * kAcross < p.channels) store_f32<float, 4, true>(state + at[q], now.h[q]);
+      }
+    }
+    reduce_lanes<kLanes / 2, kMine>(y, lane);
+    if (lane % kSub == 0 && mine < p.channels) {
+      float v = y[0];
+      if (p.d) v = fmaf(skip, xv, v);
+      if (p.z) v *= silu(Store<T>::to_f32(now.z));
+      st_f32(static_cast<T*>(p.out) + seq * p.out_s + mine, v);
+    }
+  }
+}
+
 // -------------------------------- launches -------------------------------------
 
 // The widest access that a tensor's rows allow: base, row stride, tile width and
@@ -742,8 +838,6 @@ int access_bytes(const void* p, const long long* stride, long long cols_a, long 
   }
   return 0;
 }
-
-constexpr int kSms = 148;
 
 template <typename T, int kStates, int kLanes, bool kFull>
 cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
@@ -817,6 +911,16 @@ cudaError_t step_typed(StepArgs p, cudaStream_t s) {
       return cudaGetLastError();
     };
     constexpr int kMine = l() < kStepMine ? l() : kStepMine;
+    if constexpr (kMine > 1) {
+      // Five blocks an SM, each through two sequences or more (192 sequences of 4096
+      // channels, 16 states: 20.2 us against 26.4 with a block a sequence; 64: 6.5 and 7.9;
+      // four and six blocks an SM 20.9 and 27.8).
+      const long long walk = (long long)kSms * kWalkBlocks / grid.x;
+      if (mine > 1 && vec && p.bc_vec && p.states <= 4 * lanes && walk > 0 && 2 * walk <= p.n) {
+        scan_step_walk_kernel<T, l(), kMine><<<dim3(grid.x, (unsigned)walk), kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+      }
+    }
     if (mine > 1) return vec ? run(scan_step_kernel<T, l(), kMine, true>) : run(scan_step_kernel<T, l(), kMine, false>);
     return vec ? run(scan_step_kernel<T, l(), 1, true>) : run(scan_step_kernel<T, l(), 1, false>);
   };

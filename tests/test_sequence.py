@@ -398,6 +398,21 @@ def test_scan_cut_into_chunks(lens, packed, s, d):
 @pytest.mark.parametrize("n,d,s,g", [(1, 1, 1, 1), (1, 2048, 16, 1), (3, 20, 11, 2), (5, 64, 128, 4), (9, 33, 200, 1),
                                      (70, 24, 16, 1), (2, 7, 4, 1), (4, 12, 256, 3)])
 def test_scan_step(dtype, n, d, s, g):
+    check_scan_step(dtype, n, d, s, g)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d,s,g", [
+    (30, 2048, 16, 1), (50, 1000, 20, 1), (20, 500, 200, 1), (60, 1000, 10, 1),      # four channels a turn
+    (100, 2048, 16, 1), (200, 1000, 12, 1), (64, 1024, 128, 8), (400, 512, 8, 2),    # blocks that walk over sequences
+    (120, 1020, 16, 3),                                                              # groups that a warp's channels straddle
+])
+def test_large_scan_steps(dtype, n, d, s, g):
+    check_scan_step(dtype, n, d, s, g)
+
+
+def check_scan_step(dtype, n, d, s, g):
     normal, dt = draws(n + d + s), TYPES[dtype]
     torch.manual_seed(s)
     t = scan_inputs(normal, (n,), d, s, g, dt, gap=3 if n == 3 else 0)
@@ -809,3 +824,18 @@ def test_kernels_are_timed_by_name():
     dc.conv1d_causal(t["x"], normal(16, 4, dtype=torch.bfloat16))
     times = B.profile_end()
     assert times["selective_scan"][0] == 1 and times["causal_conv"][0] == 1
+
+
+@gpu
+def test_conv_long_walks():
+    """Calls large enough for walks of 64, 32 and 16 rows."""
+    check_conv(torch.bfloat16, 4, 4096, [3001, 3001], False, True, True, True, gap=64)
+    check_conv(torch.float16, 3, 4096, [700, 0, 1, 1500, 897], True, True, False, True, tail=2)
+    check_conv(torch.float32, 4, 512, [3000, 31, 33, 2, 3134], True, False, True, False, tail=1)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scan_more_blocks_than_sms(dtype):
+    check_scan(TYPES[dtype], 40, 16, 1, [70] * 90, False, True)
+    check_scan(TYPES[dtype], 2400, 16, 1, [33, 100, 0, 64], True, False, tail=1)
