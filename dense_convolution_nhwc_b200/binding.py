@@ -87,7 +87,8 @@ class CausalConvDesc(ctypes.Structure):
 
 class ScanDesc(ctypes.Structure):
     """selective_scan_desc_t, its stride arrays' elements as fields of their own."""
-    _fields_ = [(name, ctypes.c_int) for name in ("n", "l", "d", "s", "groups", "softplus", "carry", "state_slots")] + \
+    _fields_ = [(name, ctypes.c_int) for name in ("n", "l", "d", "s", "groups", "softplus", "carry", "state_slots",
+                                              "packed")] + \
                [(f"{name}_stride_{of}", ctypes.c_longlong) for name in ("x", "dt", "z", "b", "c", "out")
                 for of in ("batch", "token")]
 

@@ -1124,6 +1124,7 @@ conv_status_t check_scan_tensors(const selective_scan_tensors_t* t, const select
   const long long n = t->offsets ? 1 : d->n, l = step ? 1 : d->l, gs = (long long)d->groups * d->s;
   if (!t->a || (l > 0 && (!t->x || !t->dt || !t->b || !t->c || !t->out))) return CONV_ERR_INVALID;
   if (!t->state && (step || d->carry || t->slots)) return CONV_ERR_INVALID;
+  if ((t->offsets != nullptr) != (d->packed != 0)) return CONV_ERR_INVALID;
   if (t->state && d->state_slots < (t->slots ? 1 : d->n)) return CONV_ERR_INVALID;
   for (const void* p : {t->x, t->dt, t->b, t->c, t->z, (const void*)t->out})
     if (!multiple_of(p, esz)) return CONV_ERR_ALIGNMENT;

@@ -960,7 +960,14 @@ ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   // Two blocks an SM are enough, and a chunk's start is worked out from all chunks
   // before it, so not too many (16384 tokens of 32 channels: 27.5 us in 148 chunks,
   // 38.6 in 256) nor too short ones.
-  const long long want = blocks > 0 ? 2LL * sm_count / blocks : 0, most = (d.l + kLeastChunk - 1LL) / kLeastChunk;
+  // Packed sequences share their rows, and the longest decides: chunks of the size
+  // that cuts all of them together into as many (a shorter sequence is one chunk, gone
+  // over once), from half the device idle on.  Chunks past a sequence's end still cost
+  // a block each, so sixteen times as many at most.  11 sequences in 10813 rows: of 48
+  // channels 65 us cut as if each had all the rows, 19.7 so; of 300 uncut 135, so 81.
+  long long want = blocks > 0 ? 2LL * sm_count / blocks : 0;
+  if (d.packed && want >= 2) want *= d.n < 16 ? d.n : 16;
+  const long long most = (d.l + kLeastChunk - 1LL) / kLeastChunk;
   long long chunks = want < most ? want : most;
   if (chunks > kMostChunks) chunks = kMostChunks;
   if (chunks >= 4) {

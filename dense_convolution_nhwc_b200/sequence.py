@@ -213,7 +213,7 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=False,
     yp, ys = _rows(out, "out", shape, dtype, index)
     t = len(shape) - 2                                  # the token dimension; a packed call has no batch before it
     batch = (lambda st: 0) if packed else (lambda st: st[0])
-    desc = B.ScanDesc(n, shape[t], dim, s, g, 1 if softplus else 0, 1 if carry else 0, have, batch(xs), xs[t], batch(ts),
+    desc = B.ScanDesc(n, shape[t], dim, s, g, 1 if softplus else 0, 1 if carry else 0, have, 1 if packed else 0, batch(xs), xs[t], batch(ts),
                       ts[t], batch(zs), zs[t], batch(bs), bs[t], batch(cs), cs[t], batch(ys), ys[t])
     need = B._selective_scan_workspace_size(byref(desc), code, index)
     if workspace is not None:
@@ -249,7 +249,7 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, sof
     if out is None:
         out = _empty_like(x, memory_format=_CONTIGUOUS)
     yp, ys = _rows(out, "out", shape, dtype, index)
-    desc = B.ScanDesc(n, 1, dim, s, g, 1 if softplus else 0, 1, have, xs[0], 0, ts[0], 0, zs[0], 0, bs[0], 0, cs[0], 0,
+    desc = B.ScanDesc(n, 1, dim, s, g, 1 if softplus else 0, 1, have, 0, xs[0], 0, ts[0], 0, zs[0], 0, bs[0], 0, cs[0], 0,
                       ys[0], 0)
     tensors = B.ScanTensors(xp, tp, bp, cp, zp, ap, dp, up, 0, ip, sp, yp)
     _enqueue(B._selective_scan_step_forward, index, byref(tensors), byref(desc), code)

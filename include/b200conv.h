@@ -280,6 +280,7 @@ B200CONV_API conv_status_t conv1d_causal_step_forward(const void *x, const void 
 typedef struct {
     int n, l, d, s, groups;               /* channels d, states 1 <= s <= 256, groups divides d */
     int softplus, carry, state_slots;
+    int packed;                           /* != 0 exactly when offsets are given: the plan goes by it */
     long long x_stride[2], dt_stride[2], z_stride[2], b_stride[2], c_stride[2], out_stride[2];
 } selective_scan_desc_t;
 

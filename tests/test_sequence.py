@@ -62,7 +62,7 @@ def test_conv_pointer_refusals():
 
 
 def scan_desc(**over):
-    d = dict(n=2, l=5, d=8, s=16, groups=2, softplus=1, carry=1, state_slots=2, x_stride=(40, 8), dt_stride=(40, 8),
+    d = dict(n=2, l=5, d=8, s=16, groups=2, softplus=1, carry=1, state_slots=2, packed=0, x_stride=(40, 8), dt_stride=(40, 8),
              z_stride=(40, 8), b_stride=(160, 32), c_stride=(160, 32), out_stride=(40, 8))
     d.update(over)
     return B.ScanDesc(*flat(d))
@@ -90,7 +90,7 @@ def test_scan_descriptor_refusals(over, status):
 @pytest.mark.parametrize("over,status", [
     (dict(x=0), 1), (dict(dt=0), 1), (dict(a=0), 1), (dict(b=0), 1), (dict(c=0), 1), (dict(out=0), 1), (dict(state=0), 1),
     (dict(x=0x100002), 3), (dict(a=0x600002), 3), (dict(state=0xb00002), 3),
-    (dict(out=0x100000), 1), (dict(out=0x100040), 1), (dict(out=0xb00000), 1), (dict(state=0x600000), 1),
+    (dict(offsets=0xd00000), 1), (dict(out=0x100000), 1), (dict(out=0x100040), 1), (dict(out=0xb00000), 1), (dict(state=0x600000), 1),
 ])
 def test_scan_pointer_refusals(over, status):
     assert B.selective_scan_forward(scan_tensors(**over), scan_desc(), 0, 0, 0, 0) == status
@@ -122,6 +122,11 @@ def test_scan_plan_is_a_rule_on_sizes():
         p = scan_plan(n=n, d=d, groups=1, l=l)
         assert p["chunks"] > 2 and (p["chunks"] - 1) * p["chunk_tokens"] < l <= p["chunks"] * p["chunk_tokens"]
         assert p["workspace_bytes"] >= n * p["chunks"] * d * 17 * 4
+    # packed sequences share the rows: shorter chunks, more of them a sequence at most
+    dense, packed = scan_plan(n=11, d=48, groups=1, l=10813), scan_plan(n=11, d=48, groups=1, l=10813, packed=1)
+    assert 2 < dense["chunks"] < packed["chunks"] <= 128 and packed["chunk_tokens"] >= 64
+    assert scan_plan(n=200, d=4096, groups=1, l=10000, packed=1)["chunks"] == 1
+    assert scan_plan(n=11, d=300, groups=1, l=10813, packed=1)["chunks"] > 4
     assert scan_plan(n=1, d=8, groups=1, l=1)["chunks"] == 1
     assert scan_plan(n=1, d=8, groups=1, l=0)["chunks"] == 1
     assert scan_plan(n=1, d=8, groups=1, l=2 ** 30)["chunk_tokens"] > 0
@@ -386,7 +391,7 @@ def test_scan_slots():
 @pytest.mark.parametrize("lens,packed", [([700], False), ([530, 530], False), ([400, 0, 3, 333, 64, 65], True)])
 @pytest.mark.parametrize("s,d", [(16, 24), (7, 10), (64, 6)])
 def test_scan_cut_into_chunks(lens, packed, s, d):
-    desc = B.ScanDesc(len(lens), sum(lens) if packed else lens[0], d, s, 1)
+    desc = B.ScanDesc(len(lens), sum(lens) + 3 if packed else lens[0], d, s, 1, packed=int(packed))
     assert B.selective_scan_workspace_size(desc, 0, 0) > 0
     for carry in (False, True):
         check_scan(torch.float32, d, s, 1, lens, packed, carry, tail=3 if packed else 0)
@@ -714,7 +719,7 @@ def test_many_short_sequences():
 @gpu
 @pytest.mark.parametrize("lens,slots", [([300, 0, 5, 270], [5, -1, 0, 2]), ([500, 40], [7, 1])])
 def test_cut_scan_with_slots(lens, slots):
-    assert B.selective_scan_workspace_size(B.ScanDesc(len(lens), sum(lens) + 2, 12, 16, 2), 0, 0) > 0
+    assert B.selective_scan_workspace_size(B.ScanDesc(len(lens), sum(lens) + 2, 12, 16, 2, packed=1), 0, 0) > 0
     for carry in (False, True):
         check_scan(torch.float16, 12, 16, 2, lens, True, carry, tail=2, slots=slots, gap=3)
 
