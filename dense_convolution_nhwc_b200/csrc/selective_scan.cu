@@ -12,7 +12,7 @@
 // Prompts.  The floor is the exponentials: one a (token, channel, state) and four
 // more a (token, channel) for softplus and gate, 16 a clock and SM in the
 // special-function units.  8192 tokens of 4096 channels and 16 states are 671 million,
-// 150 us; their 270 MB of io would take 41 us.  What the kernel spends its time on
+// 144 us; their 270 MB of io would take 41 us.  What the kernel spends its time on
 // besides is issue slots and shared-memory reads, so both are kept down:
 //  * kLanes lanes share a channel, kStates states each in registers; four states a
 //    lane (of 16) read b, c and delta a quarter as often as one would.
@@ -27,9 +27,9 @@
 //    scanners are at this one.  Done by the scanning warps themselves between their
 //    tiles, the call took 393 us.  b becomes fp32 pairs on the way, c stays as it comes:
 //    both in fp32 the shared-memory reads bound the kernel, neither the conversions do.
-// 8192 tokens of 4096 bf16 channels: 309 us (49 % of the exponentials' rate; one block an
+// 8192 tokens of 4096 bf16 channels: 309 us (47 % of the special functions' rate; one block an
 // SM, bound by the latency of one scanning warp a scheduler: 72 clocks a token).  16
-// sequences of 512 tokens: 239 us (63 %).
+// sequences of 512 tokens: 239 us (60 %).
 //
 // A call with too few channels to fill the device cuts the sequences into chunks: a
 // first launch leaves each chunk's final state from zero and its sum of delta in the
@@ -941,9 +941,9 @@ constexpr int kLeastChunk = 64, kMostChunks = 128;
 // Pure in the descriptor and the device's SM count.
 ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   ScanPlan plan{};
-  // Four states a lane: with two the smem reads of b, c and delta bound the kernel
-  // (8192 tokens of 4096 channels, 16 states: 359 us on 8 lanes, 322 on 4; 16 sequences
-  // of 512 tokens 338 and 251).
+  // Four states a lane: with two the shared-memory reads of b, c and delta bound the
+  // kernel (8192 tokens of 4096 channels, 16 states: 359 us on 8 lanes where 4 took 322;
+  // 16 sequences of 512 tokens 338 and 251).
   plan.states_per_lane = d.s <= 8 ? 2 : 4;
   plan.lanes = 4;
   while (plan.lanes * plan.states_per_lane < d.s) {
@@ -956,7 +956,7 @@ ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
   plan.chunks = 1;
   // Cut, every token is gone over twice: it pays from four chunks on (8192 tokens of
-  // 2048 channels, 4 chunks: 242 us against 322; of 3000, 3 chunks: 355 against 338).
+  // 2048 channels, 4 chunks: 242 us against 322; 2048 of 3000, 3 chunks: 89 against 84).
   // Two blocks an SM are enough, and a chunk's start is worked out from all chunks
   // before it, so not too many (16384 tokens of 32 channels: 27.5 us in 148 chunks,
   // 38.6 in 256) nor too short ones.
