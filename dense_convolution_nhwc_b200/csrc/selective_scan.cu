@@ -34,7 +34,7 @@
 // A call with too few channels to fill the device cuts the sequences into chunks: a
 // first launch leaves each chunk's final state from zero and its sum of delta in the
 // workspace, and every chunk of the second folds those before it into its first state
-// (the decay over a chunk is exp(a sum delta)).  That doubles the exponentials.  16384
+// (the decay over a chunk is exp(a sum delta), see fold).  That doubles the exponentials.  16384
 // tokens of 96 fp32 channels: 35 us.
 #include <cuda_runtime.h>
 
@@ -52,7 +52,7 @@ struct ScanArgs {
   const int *offsets, *slots;
   float* state;
   void* out;
-  float *ws_state, *ws_sum;    // chunked: [n][chunks][D][S] states (0: the first, j + 1: after chunk j from zero), [n][chunks][D] sums
+  float *ws_state, *ws_sum;    // chunked: [n][chunks][D][S] states (0: the first, j + 1: after chunk j from zero), [n][chunks][D] thirds of sums
   int n, l, channels, states, groups, state_slots, softplus, carry;
   long long x_s[2], dt_s[2], z_s[2], b_s[2], c_s[2], out_s[2];
   int chunk, chunks;           // tokens a chunk (a multiple of 64), chunks a sequence
@@ -287,6 +287,17 @@ __device__ __forceinline__ void load_states(const T* p, float (&v)[kStates]) {
   for (int i = 0; i < kStates; ++i) v[i] = Store<T>::to_f32(e[i]);
 }
 
+// The state after a chunk that was entered with h and that ends with `from` when it is
+// entered with zero: exp(a sum delta) h + from.  Over a chunk the exponent leaves fp32's
+// range where no token's does, so the decay comes as three factors of a third of it,
+// each kept within 2^-120 .. 2^120.  Past that the product of a nonzero h (2^-149 at
+// least) overflows and that of a finite one vanishes as it should; a state of zero stays
+// zero and an infinite one infinite, as they do token by token.
+__device__ __forceinline__ float fold(float a, float third_of_sum, float h, float from) {
+  const float e = ex2(fminf(fmaxf(fmaf(a, third_of_sum, kEx2Bias), -120.0f), 120.0f));
+  return fmaf(e, e * (e * h), from);
+}
+
 // kFull: states == kStates * kLanes.  kEnds: the chunk's final state from zero and its sum of delta, no output.
 template <typename T, int kStates, int kLanes, bool kFull, bool kEnds, int kBlocks>
 __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) scan_kernel(const ScanArgs p) {
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) sc
         float all = 0.0f;
 #pragma unroll
         for (int i = 0; i < L::kHelpers / 32; ++i) all += sums[i * L::kChannels + c];
-        p.ws_sum[((long long)w.seq * p.chunks + chunk) * p.channels + w.ch + c] = all;
+        p.ws_sum[((long long)w.seq * p.chunks + chunk) * p.channels + w.ch + c] = all * (1.0f / 3.0f);
       }
     }
     return;
@@ -512,7 +523,7 @@ __global__ void __launch_bounds__(Shape<T, kStates, kLanes>::kBlock, kBlocks) sc
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
         for (int i = 0; i < kStates; ++i)
-          if (j + u < chunk && i < have) h[i] = fmaf(decay(a2[i].x, sum[u]), h[i], from[u][i]);
+          if (j + u < chunk && i < have) h[i] = fold(a2[i].x, sum[u], h[i], from[u][i]);
     }
   } else if (p.carry) {
 #pragma unroll
