@@ -49,12 +49,13 @@ __device__ __forceinline__ bool my_place(int groups, int* group, long long* item
   return *group < groups;
 }
 
+// silu of values above kFar.
 template <int V>
-__device__ __forceinline__ void silu_all(float (&v)[V]) {
+__device__ __forceinline__ void silu_near_all(float (&v)[V]) {
   if constexpr (V % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
-      const float2 y = silu(make_float2(v[i], v[i + 1]));
+      const float2 y = silu_near(make_float2(v[i], v[i + 1]));
       v[i] = y.x;
       v[i + 1] = y.y;
     }
@@ -62,6 +63,14 @@ __device__ __forceinline__ void silu_all(float (&v)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
   }
+}
+
+// The outputs whose sums are far out, over those that silu_near_all gave.
+template <typename T, int V>
+__device__ __forceinline__ void put_far(const float (&sums)[V], T* out) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (sums[i] < kFar) st_f32(out + i, silu_far(sums[i]));
 }
 
 // The taps of V channels: [V][K] in memory, [K][V] in registers.
@@ -123,14 +132,18 @@ struct Walk {
     }
   }
 
-  // The next output from the window and the row after it, which the window takes up.
-  __device__ __forceinline__ void step(float (&win)[K - 1][V], const float (&now)[V], float (&acc)[V]) const {
+  // The next output from the window and the row after it, which the window takes up;
+  // low: the lowest sum so far, where it matters.
+  __device__ __forceinline__ void step(float (&win)[K - 1][V], const float (&now)[V], float (&acc)[V], float& low) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = b[v];
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) multiply_add<V>(w[k], win[k], acc);
     multiply_add<V>(w[K - 1], now, acc);
-    if (p.silu) silu_all<V>(acc);
+    if (p.silu) {
+      low = lowest<V>(acc, low);
+      silu_near_all<V>(acc);
+    }
 #pragma unroll
     for (int k = 0; k < K - 1; ++k)
 #pragma unroll
@@ -140,7 +153,7 @@ struct Walk {
   // Positions [from, to) of the sequence whose rows start at x and out.
   __device__ __forceinline__ void run(const T* x, T* out, int from, int to, int slot) const {
     if (from >= to) return;
-    float win[K - 1][V];
+    float win[K - 1][V], low = 0.0f;
     const T* ahead = x + from * p.x_st;
     T* here = out + from * p.o_st;
     if constexpr (VEC) {
@@ -174,7 +187,7 @@ struct Walk {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           float acc[V];
-          step(win, now[u], acc);
+          step(win, now[u], acc, low);
           if (at + u < to) store_f32<T, V, true>(here, acc);
           here += p.o_st;
         }
@@ -202,7 +215,7 @@ struct Walk {
           float acc[V], now[V];
 #pragma unroll
           for (int v = 0; v < V; ++v) now[v] = Store<T>::to_f32(in[u][v]);
-          step(win, now, acc);
+          step(win, now, acc, low);
           if (at + u < to) store_f32<T, V, false>(here, acc);
           here += p.o_st;
         }
@@ -211,6 +224,24 @@ struct Walk {
 #pragma unroll
           for (int v = 0; v < V; ++v) in[u][v] = next[u][v];
       }
+    }
+    if (low < kFar) far(x, out, from, to, slot);
+  }
+
+  // Once more over rows of which some have sums far out.  What they read is as it was:
+  // the old window is replaced after the walk that reads it.
+  __device__ __forceinline__ void far(const T* x, T* out, int from, int to, int slot) const {
+#pragma unroll 1
+    for (int t = from; t < to; ++t) {
+      float sums[V], v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[i] = b[i];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        row(x, t - (K - 1) + k, slot, v);
+        multiply_add<V>(w[k], v, sums);
+      }
+      put_far<T, V>(sums, out + t * p.o_st);
     }
   }
 
@@ -322,8 +353,13 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(const StepAr
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[v] = fmaf(w[k][v], win[k][v], acc[v]);
   }
-  if (p.silu) silu_all<V>(acc);
-  store_f32<T, V, VEC>(static_cast<T*>(p.out) + seq * p.o_sn + ch, acc);
+  T* out = static_cast<T*>(p.out) + seq * p.o_sn + ch;
+  float sums[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sums[v] = acc[v];
+  if (p.silu) silu_near_all<V>(acc);
+  store_f32<T, V, VEC>(out, acc);
+  if (p.silu && lowest<V>(sums, 0.0f) < kFar) put_far<T, V>(sums, out);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) store_f32<T, V, VEC>(state + (long long)k * p.c, win[k + 1]);
 }

@@ -110,3 +110,111 @@ def test_infinite_states_through_decaying_chunks(carried):
         assert (y[first:, 2] == float("inf")).all() and (h[2] == float("inf")).all()
         others = [i for i in range(24) if i != 2]
         assert y[:, others].isfinite().all() and h[others].isfinite().all() and y[:first].isfinite().all()
+
+
+# -------------------------------- silu, far out ---------------------------------
+#
+# exp(-v) leaves fp32's range from v = -88.7 on, and the reciprocal of 1 + exp(-v) from
+# -87.3, where silu(v) is still a normal number (down to -91.9; above 2^-149 to -108).
+# The reference's bound is relative, with the type's smallest step at the final
+# rounding (2^-149 of fp32).  A gate's sigmoid, and for steps the gate, is held in fp32
+# before it is multiplied on.  Below 2^-126, for z < -87.3, that is a multiple of 2^-149
+# and off by up to 2^-150, which the z and the 0.75 that it meets here multiply.
+
+FAR = [-80.0, -84.0, -87.0, -87.5, -88.0, -88.75, -89.0, -90.0, -91.5, -92.0, -95.0, -100.0, -103.0, -104.0, -106.0, -112.0,
+       -130.0, -1e4, -1e30, 80.0, 88.0, 100.0, 1e4, 1e30, 0.0, -0.0, 2.0 ** -120, -2.0 ** -120, -1.0, 1.0, -20.0, 20.0]
+
+
+def far_values(dtype):
+    """Each of FAR beside ordinary values, and in the place of both neighbours of a pair."""
+    v = torch.tensor(FAR)
+    v = v[v.abs() <= torch.finfo(dtype).max]
+    return torch.cat([v, v.repeat_interleave(2), torch.stack([v, torch.full_like(v, 0.5)]).T.flatten()]).to(dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [0, 3])
+def test_activation_far_out(dtype, width):
+    """silu of a conv that passes its input on, over prompts and steps, 16-byte accesses and single elements."""
+    v = far_values(TYPES[dtype])
+    v = v[:v.numel() // 8 * 8 - width]
+    w = torch.tensor([0.0, 1.0]).repeat(v.numel(), 1).to(v.dtype)
+    y, bound = ref._silu(v.double()[None], torch.zeros(1, v.numel(), dtype=torch.float64))      # 0 x' + 1 x is exact
+    bound = ref._cast(y, bound, v.dtype)
+    got = dc.conv1d_causal(v.cuda()[None, None], w.cuda(), activation="silu")
+    ref.assert_within(got[0], y, bound, "prompt")
+    got = dc.conv1d_causal_step(v.cuda()[None], w.cuda(), torch.zeros(1, 1, v.numel(), dtype=v.dtype, device="cuda"),
+                                activation="silu")
+    ref.assert_within(got, y, bound, "step")
+
+
+def held(z):
+    return torch.where(z < -87.3, 0.75 * z.double().abs() * 2.0 ** -150, 0.0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 64])
+def test_gate_far_out(dtype, n):
+    """silu(z) 0.75: b is zero and d x is 0.75, over prompts and steps (64: blocks that walk over sequences)."""
+    z = far_values(TYPES[dtype])
+    dim, s = z.numel(), 16
+    one = dict(x=torch.ones(1, dim), dt=torch.zeros(1, dim), b=torch.zeros(1, 1, s), c=torch.ones(1, 1, s), z=z[None])
+    one = {name: v.to(z.dtype) for name, v in one.items()}
+    fixed = dict(a=-torch.ones(dim, s), d=torch.full((dim,), 0.75))
+    y, bound, _, _ = ref.scan(**one, **fixed, dt_bias=None, softplus=True, h=torch.zeros(dim, s))
+    bound = bound + held(one["z"])
+    fixed = {name: v.cuda() for name, v in fixed.items()}
+    many = {name: v.cuda().expand(n, *v.shape[1:]).contiguous() for name, v in one.items()}
+    got = dc.selective_scan(**{name: v[:, None] for name, v in many.items()}, **fixed, softplus=True)
+    ref.assert_within(got[:, 0], y.expand(n, dim), bound.expand(n, dim), "prompt")
+    got = dc.selective_scan_step(**many, **fixed, state=torch.zeros(n, dim, s, device="cuda"), softplus=True)
+    ref.assert_within(got, y.expand(n, dim), bound.expand(n, dim), "step")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("c", [24, 21])
+@pytest.mark.parametrize("carry", [False, True])
+def test_activations_far_out_anywhere_in_a_prompt(dtype, c, carry):
+    """Whole and half numbers, whose sums are exact: some 15 % of them lie below -80, in
+    the first rows that read the old window, at a sequence's end, between two walks."""
+    g = torch.Generator().manual_seed(11)
+    lens = [37, 3, 0, 1, 150]
+    x = torch.randint(-90, 91, (sum(lens) + 2, c), generator=g).to(TYPES[dtype])
+    w = (torch.randint(0, 2, (c, 4), generator=g) - 0.5).to(x.dtype)
+    w[:, 3] = 1
+    bias = torch.randint(-4, 5, (c,), generator=g).to(x.dtype)
+    window = torch.randint(-90, 91, (len(lens), 3, c), generator=g).to(x.dtype)
+    offsets = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    state, out = window.cuda(), torch.full_like(x, 7.0, device="cuda")
+    dc.conv1d_causal(x.cuda(), w.cuda(), bias.cuda(), "silu", offsets=torch.tensor(offsets, dtype=torch.int32).cuda(),
+                     state=state, carry=carry, out=out)
+    far = 0
+    for i, lo in enumerate(offsets[:-1]):
+        old = window[i] if carry else torch.zeros_like(window[i])
+        rows = x[lo:lo + lens[i]]
+        v, _, kept = ref.causal_conv(rows, w, bias, False, old)
+        y, bound = ref._silu(v, torch.zeros_like(v))
+        far += int((v < -87.4).sum())
+        ref.assert_within(out[lo:lo + lens[i]], y, ref._cast(y, bound, x.dtype), f"sequence {i}")
+        assert torch.equal(state[i].cpu(), kept)
+    assert far > 200 and (out[offsets[-1]:] == 7).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [40, 37])
+def test_gates_far_out_anywhere_in_a_prompt(dtype, dim):
+    """Several tiles of tokens, whole vectors of channels and the ends of them."""
+    far, g = far_values(TYPES[dtype]), torch.Generator().manual_seed(13)
+    z = far[torch.randint(0, far.numel(), (2, 75, dim), generator=g)]
+    t = dict(x=torch.ones(2, 75, dim), dt=torch.zeros(2, 75, dim), b=torch.zeros(2, 75, 1, 16), c=torch.ones(2, 75, 1, 16), z=z)
+    t = {name: v.to(z.dtype) for name, v in t.items()}
+    fixed = dict(a=-torch.ones(dim, 16), d=torch.full((dim,), 0.75))
+    got = dc.selective_scan(**{name: v.cuda() for name, v in (t | fixed).items()}, softplus=True)
+    for i in range(2):
+        part = {name: v[i] for name, v in t.items()}
+        y, bound, _, _ = ref.scan(**part, **fixed, dt_bias=None, softplus=True, h=torch.zeros(dim, 16))
+        ref.assert_within(got[i], y, bound + held(z[i]), f"sequence {i}")
