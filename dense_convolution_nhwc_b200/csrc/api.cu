@@ -1070,12 +1070,15 @@ Span span_of(const void* p, long long n, long long l, const long long* stride, l
 }
 bool meets(const Span& a, const Span& b) { return overlaps(a.p, a.bytes, b.p, b.bytes); }
 
-// Rows that are written must not overlap each other; rows that are read may (a broadcast).
+// Rows that are written must not overlap each other, nested either way (the tokens of a
+// sequence within its own span, or the sequences of a token within the token's); rows
+// that are read may (a broadcast).
 bool valid_strides(const long long* s, long long n, long long l, long long cols, bool written) {
   if (s[0] < 0 || s[1] < 0) return false;
-  if (!written) return true;
-  if (l > 1 && s[1] < cols) return false;
-  return n <= 1 || s[0] >= (l - 1) * s[1] + cols;
+  if (!written || n < 1 || l < 1) return true;
+  if (n == 1) return l == 1 || s[1] >= cols;
+  if (l == 1) return s[0] >= cols;
+  return (s[1] >= cols && s[0] >= (l - 1) * s[1] + cols) || (s[0] >= cols && s[1] >= (n - 1) * s[0] + cols);
 }
 
 conv_status_t check_causal(const conv1d_causal_desc_t* d, conv_dtype_t dt, bool state, bool slots) {

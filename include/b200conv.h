@@ -233,7 +233,9 @@ B200CONV_API conv_status_t conv1d_forward(const void *in, const void *w, void *o
  *    batch stride is not read).  Sequences may be empty.  Rows outside every
  *    sequence are neither read nor written.  Offsets are clamped to [0, l]: a
  *    bad list gives unspecified results, never an access outside the tensors.
- *  - Strides are in elements; the channels of a row are contiguous.  Any
+ *  - Strides are in elements; the channels of a row are contiguous.  The rows of
+ *    inputs may overlap (a batch stride of 0, say); those of out may not, and lie
+ *    sequence by sequence or token by token ([L, N, C] buffers), with any gaps.  Any
  *    alignment is accepted; 16-byte aligned bases, strides and widths run
  *    fastest.  Pointers must be multiples of their element size, else
  *    CONV_ERR_ALIGNMENT.

@@ -6,7 +6,8 @@ import torch
 import dense_convolution_nhwc_b200 as dc
 from dense_convolution_nhwc_b200 import binding as B
 from tests import sequence_ref as ref
-from tests.test_sequence import TYPES, cpu, draws, scan_inputs
+from tests.test_sequence import (BIAS, OUT, STATE, TYPES, W, X, conv_desc, cpu, draws, scan_desc, scan_inputs,
+                                 scan_tensors)
 
 B200 = B.DeviceProps(148, 10, 0, 183359 * 2 ** 20)
 gpu = pytest.mark.gpu
@@ -218,3 +219,33 @@ def test_gates_far_out_anywhere_in_a_prompt(dtype, dim):
         part = {name: v[i] for name, v in t.items()}
         y, bound, _, _ = ref.scan(**part, **fixed, dt_bias=None, softplus=True, h=torch.zeros(dim, 16))
         ref.assert_within(got[i], y, bound + held(z[i]), f"sequence {i}")
+
+
+# ------------------------------- layouts of out ---------------------------------
+
+@pytest.mark.parametrize("stride", [(8, 15), (15, 8), (7, 40), (40, 7), (0, 8), (8, 8), (39, 8), (8, 0)])
+def test_rows_of_out_may_not_overlap(stride):
+    """Two sequences of five rows of eight: neither within its own span."""
+    assert B.conv1d_causal_forward(X, W, BIAS, 0, STATE, 0, OUT, conv_desc(out_stride=stride), 0, 0) == 1
+    assert B.selective_scan_forward(scan_tensors(), scan_desc(out_stride=stride), 0, 0, 0, 0) == 1
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,gap", [(24, 0), (24, 8), (21, 3)])
+def test_out_token_by_token(dtype, dim, gap):
+    """Outputs, and inputs, that are transposed [L, N, C] buffers."""
+    normal, n, l = draws(15), 3, 70
+    torch.manual_seed(15)
+    buffer = torch.full((l, n, dim + gap), 7.0, dtype=TYPES[dtype], device="cuda")
+    out = buffer[..., :dim].transpose(0, 1)
+    x, w = normal(n, l, dim, dtype=buffer.dtype), normal(dim, 4, dtype=buffer.dtype)
+    want = dc.conv1d_causal(x, w, activation="silu")
+    across = x.transpose(0, 1).contiguous().transpose(0, 1)
+    assert dc.conv1d_causal(across, w, activation="silu", out=out) is out
+    assert torch.equal(out, want) and (buffer[..., dim:] == 7).all()
+    t = scan_inputs(normal, (n, l), dim, 16, 1, buffer.dtype)
+    want = dc.selective_scan(**t, softplus=True)
+    buffer.fill_(7.0)
+    dc.selective_scan(**dict(t, x=t["x"].transpose(0, 1).contiguous().transpose(0, 1)), softplus=True, out=out)
+    assert torch.equal(out, want) and (buffer[..., dim:] == 7).all()
