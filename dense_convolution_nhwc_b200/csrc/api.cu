@@ -1072,10 +1072,13 @@ bool meets(const Span& a, const Span& b) { return overlaps(a.p, a.bytes, b.p, b.
 
 // Rows that are written must not overlap each other, nested either way (the tokens of a
 // sequence within its own span, or the sequences of a token within the token's); rows
-// that are read may (a broadcast).
+// that are read may (a broadcast).  No tensor reaches over 2^60 elements, so that spans
+// are exact in 64 bits.
 bool valid_strides(const long long* s, long long n, long long l, long long cols, bool written) {
   if (s[0] < 0 || s[1] < 0) return false;
-  if (!written || n < 1 || l < 1) return true;
+  if (n < 1 || l < 1) return true;
+  if ((__int128)(n - 1) * s[0] + (__int128)(l - 1) * s[1] + cols > (__int128)1 << 60) return false;
+  if (!written) return true;
   if (n == 1) return l == 1 || s[1] >= cols;
   if (l == 1) return s[0] >= cols;
   return (s[1] >= cols && s[0] >= (l - 1) * s[1] + cols) || (s[0] >= cols && s[1] >= (n - 1) * s[0] + cols);

@@ -230,6 +230,18 @@ def test_rows_of_out_may_not_overlap(stride):
     assert B.selective_scan_forward(scan_tensors(), scan_desc(out_stride=stride), 0, 0, 0, 0) == 1
 
 
+@pytest.mark.parametrize("stride", [(2 ** 62, 8), (40, 2 ** 61), (2 ** 60, 8), (40, 2 ** 58)])
+def test_strides_past_any_memory(stride):
+    """Spans that 64 bits do not hold, or no memory has, are refused, not wrapped around."""
+    for name in ("x_stride", "out_stride"):
+        assert B.conv1d_causal_forward(X, W, BIAS, 0, STATE, 0, OUT, conv_desc(n=3, state_slots=3, **{name: stride}), 0, 0) == 1
+    for name in ("x_stride", "dt_stride", "z_stride", "b_stride", "c_stride", "out_stride"):
+        desc = scan_desc(n=3, state_slots=3, **{name: stride})
+        assert B.selective_scan_forward(scan_tensors(), desc, 0, 0, 0, 0) == 1
+    step = conv_desc(n=3, state_slots=3, x_stride=(2 ** 62, 0))
+    assert B.conv1d_causal_step_forward(X, W, 0, STATE, 0, OUT, step, 0, 0) == 1
+
+
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim,gap", [(24, 0), (24, 8), (21, 3)])
