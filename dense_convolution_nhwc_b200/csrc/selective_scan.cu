@@ -878,8 +878,11 @@ cudaError_t scan_shaped(ScanArgs p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   // With a block an SM at most, the registers of two make a better schedule (8192 tokens
-  // of 4096 channels: 309 us with 147 registers, 334 with the 128 of two blocks an SM).
-  if (kFull && blocks * p.chunks <= kSms) return run(scan_kernel<T, kStates, kLanes, kFull, false, 1>);
+  // of 4096 channels: 311 us with 147 registers, 334 with the 128 of two blocks an SM).
+  // Built for the states that fill their lanes alone.
+  if constexpr (kFull) {
+    if (blocks * p.chunks <= kSms) return run(scan_kernel<T, kStates, kLanes, kFull, false, 1>);
+  }
   return run(scan_kernel<T, kStates, kLanes, kFull, false, (L::kBytes > 110 * 1024 ? 1 : 2)>);
 }
 
