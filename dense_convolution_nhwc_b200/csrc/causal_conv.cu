@@ -25,7 +25,6 @@ namespace b200conv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 1;      // rows worked on together
 constexpr int kAhead = 8;      // rows on their way
 constexpr int kLoose = 8;      // rows loaded together where 16-byte accesses are not possible
 constexpr int kBytes = 16;     // of channels a thread
@@ -158,39 +157,30 @@ struct Walk {
     T* here = out + from * p.o_st;
     if constexpr (VEC) {
       // kAhead rows of this thread's own 16 bytes are on their way into shared memory
-      // while kBatch rows are worked on.  Only the thread itself reads them, so its
-      // own copies are all it waits for.
+      // while one is worked on.  Only the thread itself reads them, so its own copies
+      // are all it waits for.
       extern __shared__ uint4 ring[];
       uint4* mine = ring + threadIdx.y * blockDim.x + threadIdx.x;
       const int step_of = blockDim.x * blockDim.y;
       auto fetch = [&](int row_in_ring, int count) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (u < count) copy_async<16>(mine + (row_in_ring + u) * step_of, ahead);
-          ahead += p.x_st;
-        }
+        if (count > 0) copy_async<16>(mine + row_in_ring * step_of, ahead);
+        ahead += p.x_st;
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
 #pragma unroll
-      for (int f = 0; f < kAhead / kBatch; ++f) fetch(f * kBatch, to - from - f * kBatch);
+      for (int f = 0; f < kAhead; ++f) fetch(f, to - from - f);
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
-      for (int at = from, slot_in_ring = 0; at < to; at += kBatch) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / kBatch - 1) : "memory");
-        float now[kBatch][V];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          load_f32<T, V, true>(reinterpret_cast<const T*>(mine + (slot_in_ring + u) * step_of), now[u]);
+      for (int at = from, row_in_ring = 0; at < to; ++at) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        float now[V], acc[V];
+        load_f32<T, V, true>(reinterpret_cast<const T*>(mine + row_in_ring * step_of), now);
         asm volatile("" ::: "memory");       // read before the next copy into the same place is issued
-        fetch(slot_in_ring, to - at - kAhead);
-        slot_in_ring = slot_in_ring + kBatch == kAhead ? 0 : slot_in_ring + kBatch;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          float acc[V];
-          step(win, now[u], acc, low);
-          if (at + u < to) store_f32<T, V, true>(here, acc);
-          here += p.o_st;
-        }
+        fetch(row_in_ring, to - at - kAhead);
+        row_in_ring = row_in_ring + 1 == kAhead ? 0 : row_in_ring + 1;
+        step(win, now, acc, low);
+        store_f32<T, V, true>(here, acc);
+        here += p.o_st;
       }
       // a later walk of this thread reuses the ring: nothing may be on its way into it
       asm volatile("cp.async.wait_group 0;" ::: "memory");
