@@ -26,7 +26,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 8;      // rows on their way
-constexpr int kLoose = 8;      // rows loaded together where 16-byte accesses are not possible
+constexpr int kLoose = 4;      // rows loaded together where 16-byte accesses are not possible: their
+                               // sums are kept for put_far, 64 registers in all (8 rows: 122, 32 us for 26)
 constexpr int kBytes = 16;     // of channels a thread
 
 struct ConvArgs {
@@ -48,9 +49,9 @@ __device__ __forceinline__ bool my_place(int groups, int* group, long long* item
   return *group < groups;
 }
 
-// silu of values above kFar.
+// silu of the sums above kFar, and the outputs of the others.
 template <int V>
-__device__ __forceinline__ void silu_near_all(float (&v)[V]) {
+__device__ __forceinline__ void activate(float (&v)[V]) {
   if constexpr (V % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
@@ -60,11 +61,9 @@ __device__ __forceinline__ void silu_near_all(float (&v)[V]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
+    for (int i = 0; i < V; ++i) v[i] = silu_near(v[i]);
   }
 }
-
-// The outputs whose sums are far out, over those that silu_near_all gave.
 template <typename T, int V>
 __device__ __forceinline__ void put_far(const float (&sums)[V], T* out) {
 #pragma unroll
@@ -131,18 +130,13 @@ struct Walk {
     }
   }
 
-  // The next output from the window and the row after it, which the window takes up;
-  // low: the lowest sum so far, where it matters.
-  __device__ __forceinline__ void step(float (&win)[K - 1][V], const float (&now)[V], float (&acc)[V], float& low) const {
+  // The next sums from the window and the row after it, which the window takes up.
+  __device__ __forceinline__ void step(float (&win)[K - 1][V], const float (&now)[V], float (&acc)[V]) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = b[v];
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) multiply_add<V>(w[k], win[k], acc);
     multiply_add<V>(w[K - 1], now, acc);
-    if (p.silu) {
-      low = lowest<V>(acc, low);
-      silu_near_all<V>(acc);
-    }
 #pragma unroll
     for (int k = 0; k < K - 1; ++k)
 #pragma unroll
@@ -152,10 +146,11 @@ struct Walk {
   // Positions [from, to) of the sequence whose rows start at x and out.
   __device__ __forceinline__ void run(const T* x, T* out, int from, int to, int slot) const {
     if (from >= to) return;
-    float win[K - 1][V], low = 0.0f;
+    float win[K - 1][V];
     const T* ahead = x + from * p.x_st;
     T* here = out + from * p.o_st;
     if constexpr (VEC) {
+      float low = 0.0f;      // of the sums
       // kAhead rows of this thread's own 16 bytes are on their way into shared memory
       // while one is worked on.  Only the thread itself reads them, so its own copies
       // are all it waits for.
@@ -178,12 +173,17 @@ struct Walk {
         asm volatile("" ::: "memory");       // read before the next copy into the same place is issued
         fetch(row_in_ring, to - at - kAhead);
         row_in_ring = row_in_ring + 1 == kAhead ? 0 : row_in_ring + 1;
-        step(win, now, acc, low);
+        step(win, now, acc);
+        if (p.silu) {
+          low = lowest<V>(acc, low);
+          activate<V>(acc);
+        }
         store_f32<T, V, true>(here, acc);
         here += p.o_st;
       }
       // a later walk of this thread reuses the ring: nothing may be on its way into it
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (low < kFar) far(x, out, from, to, slot);
     } else {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) row(x, from - (K - 1) + j, slot, win[j]);
@@ -200,14 +200,26 @@ struct Walk {
       fetch(in, to - from);
       for (int at = from; at < to; at += kLoose) {
         fetch(next, to - at - kLoose);
+        float sums[kLoose][V], low = 0.0f;
 #pragma unroll
         for (int u = 0; u < kLoose; ++u) {
           float acc[V], now[V];
 #pragma unroll
           for (int v = 0; v < V; ++v) now[v] = Store<T>::to_f32(in[u][v]);
-          step(win, now, acc, low);
+          step(win, now, sums[u]);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = sums[u][v];
+          if (p.silu) {
+            low = lowest<V>(acc, low);
+            activate<V>(acc);
+          }
           if (at + u < to) store_f32<T, V, false>(here, acc);
           here += p.o_st;
+        }
+        if (low < kFar) {
+#pragma unroll
+          for (int u = 0; u < kLoose; ++u)
+            if (at + u < to) put_far<T, V>(sums[u], here - (kLoose - u) * p.o_st);
         }
 #pragma unroll
         for (int u = 0; u < kLoose; ++u)
@@ -215,10 +227,9 @@ struct Walk {
           for (int v = 0; v < V; ++v) in[u][v] = next[u][v];
       }
     }
-    if (low < kFar) far(x, out, from, to, slot);
   }
 
-  // Once more over rows of which some have sums far out.  What they read is as it was:
+  // Once more over the rows of a walk of which some have sums far out.  What they read is as it was:
   // the old window is replaced after the walk that reads it.
   __device__ __forceinline__ void far(const T* x, T* out, int from, int to, int slot) const {
 #pragma unroll 1
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(const StepAr
   float sums[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) sums[v] = acc[v];
-  if (p.silu) silu_near_all<V>(acc);
+  if (p.silu) activate<V>(acc);
   store_f32<T, V, VEC>(out, acc);
   if (p.silu && lowest<V>(sums, 0.0f) < kFar) put_far<T, V>(sums, out);
 #pragma unroll

@@ -94,19 +94,18 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// v / (1 + exp(-v)); -inf gives NaN as the quotient does.  Below kFar the reciprocal and
-// then exp(-v) would leave fp32's range while the quotient is in it (a normal number down
-// to -91.9).  There 1 + exp(-v) is exp(-v) to 2^-115, and the quotient is v exp(v), its
-// exponential taken 2^32 times as large so that only the last product is below 2^-126.
-constexpr float kFar = -80.0f;
-__device__ __forceinline__ float silu_far(float v) { return v * ex2(fmaf(v, kLog2e, 32.0f)) * 0x1p-32f; }
-__device__ __forceinline__ float silu(float v) { return v < kFar ? silu_far(v) : v * rcp(1.0f + ex2(-kLog2e * v)); }
-
-// Of two values, the arithmetic between the special functions packed.  In place of a test
-// the exponential comes as the square of that of half the argument, and is added to 1 as
-// 2^-32 of itself, which keeps the reciprocal in range down to v = -109.  The sigmoid itself
-// is below 2^-126 from -87.3 on and there a multiple of 2^-149: silu is off by |v| 2^-150
-// more.  (Scans with 16 sequences of 512 tokens: 240 us, with a test 246.)
+// v / (1 + exp(-v)); -inf gives NaN as the quotient does.  From v = -87.3 down the reciprocal
+// and then exp(-v) leave fp32's range while the quotient is in it (a normal number to
+// -91.9).  So the exponential comes as the square of that of half the argument, and is
+// added to 1 as 2^-32 of itself, which keeps the reciprocal in range down to -109.  The
+// sigmoid itself is then below 2^-126 and a multiple of 2^-149: the result is off by up to
+// |v| 2^-150 more.  (A test for low values in its place: scans of 16 sequences of 512
+// tokens 246 us, 240 so.)
+__device__ __forceinline__ float silu(float v) {
+  const float h = ex2(-0.5f * kLog2e * v);
+  return v * (rcp(fmaf(h * 0x1p-32f, h, 0x1p-32f)) * 0x1p-32f);
+}
+// Of two values, the arithmetic between the special functions packed.
 __device__ __forceinline__ float2 silu(float2 v) {
   auto c = [](float k) { return make_float2(k, k); };
   const float2 arg = __fmul2_rn(v, c(-0.5f * kLog2e));
@@ -115,9 +114,15 @@ __device__ __forceinline__ float2 silu(float2 v) {
   return __fmul2_rn(v, __fmul2_rn(make_float2(rcp(low.x), rcp(low.y)), c(0x1p-32f)));
 }
 
-// The same above kFar alone, for kernels bound by the way from a sum to its output: they
-// look for sums that are far out with `lowest` and put those outputs right afterwards
-// (a convolution of 50 us takes 56 with either of the forms above).
+// The same above kFar alone, for a kernel bound by the way from a sum to its output: it
+// looks for sums further out with `lowest` and puts those outputs right afterwards with
+// silu_far.  There 1 + exp(-v) is exp(-v) to 2^-115 and the quotient v exp(v), its
+// exponential taken 2^32 times as large so that only the last product is below 2^-126.
+// (A convolution of 50 us takes 56 with the form above, or with a test before the store;
+// one by single elements, 4096 rows of 4092, 28 in place of 26.)
+constexpr float kFar = -80.0f;
+__device__ __forceinline__ float silu_far(float v) { return v * ex2(fmaf(v, kLog2e, 32.0f)) * 0x1p-32f; }
+__device__ __forceinline__ float silu_near(float v) { return v * rcp(1.0f + ex2(-kLog2e * v)); }
 __device__ __forceinline__ float2 silu_near(float2 v) {
   const float2 arg = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
   const float2 low = __fadd2_rn(make_float2(ex2(arg.x), ex2(arg.y)), make_float2(1.0f, 1.0f));
