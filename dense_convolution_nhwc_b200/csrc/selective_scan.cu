@@ -55,7 +55,7 @@ struct ScanArgs {
   float *ws_state, *ws_sum;    // chunked: [n][chunks][D][S] states (0: the first, j + 1: after chunk j from zero), [n][chunks][D] thirds of sums
   int n, l, channels, states, groups, state_slots, softplus, carry;
   long long x_s[2], dt_s[2], z_s[2], b_s[2], c_s[2], out_s[2];
-  int chunk, chunks;           // tokens a chunk (a multiple of 64), chunks a sequence
+  int chunk, chunks;           // tokens a chunk (a multiple of kTile), chunks a sequence
   int tiles;                   // channel tiles a group
   int x_v, dt_v, z_v, b_v, c_v, out_v;   // bytes an access: 16, 8, 4, or 0 for single elements
 };

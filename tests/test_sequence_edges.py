@@ -6,7 +6,7 @@ import torch
 import dense_convolution_nhwc_b200 as dc
 from dense_convolution_nhwc_b200 import binding as B
 from tests import sequence_ref as ref
-from tests.test_sequence import (BIAS, OUT, STATE, TYPES, W, X, conv_desc, cpu, draws, scan_desc, scan_inputs,
+from tests.test_sequence import (BIAS, OUT, STATE, TYPES, W, X, check_scan, conv_desc, cpu, draws, scan_desc, scan_inputs,
                                  scan_tensors)
 
 B200 = B.DeviceProps(148, 10, 0, 183359 * 2 ** 20)
@@ -261,3 +261,20 @@ def test_out_token_by_token(dtype, dim, gap):
     buffer.fill_(7.0)
     dc.selective_scan(**dict(t, x=t["x"].transpose(0, 1).contiguous().transpose(0, 1)), softplus=True, out=out)
     assert torch.equal(out, want) and (buffer[..., dim:] == 7).all()
+
+
+# ----------------------- chunks that are no multiple of 64 ----------------------
+
+def test_chunks_are_whole_tiles_of_32():
+    assert chunk_tokens(1, 380, 1900, 16) == 96 and chunk_tokens(11, 10813, 48, 16, packed=True) == 96
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("carry", [False, True])
+def test_chunks_of_an_odd_number_of_tiles(dtype, carry):
+    """Four chunks of 96 tokens, the last one of 92; and packed, 97 tokens and one chunk exactly."""
+    check_scan(TYPES[dtype], 1900, 16, 1, [380], False, carry)
+    lens = [97, 0, 96, 350]
+    assert chunk_tokens(4, sum(lens) + 2, 1000, 16, packed=True) == 96
+    check_scan(TYPES[dtype], 1000, 16, 1, lens, True, carry, tail=2)
