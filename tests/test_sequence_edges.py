@@ -6,6 +6,7 @@ import torch
 import dense_convolution_nhwc_b200 as dc
 from dense_convolution_nhwc_b200 import binding as B
 from tests import sequence_ref as ref
+from tests.gpu_util import Guarded, guarded_input
 from tests.test_sequence import (BIAS, OUT, STATE, TYPES, W, X, check_scan, conv_desc, cpu, draws, scan_desc, scan_inputs,
                                  scan_tensors)
 
@@ -278,3 +279,46 @@ def test_chunks_of_an_odd_number_of_tiles(dtype, carry):
     lens = [97, 0, 96, 350]
     assert chunk_tokens(4, sum(lens) + 2, 1000, 16, packed=True) == 96
     check_scan(TYPES[dtype], 1000, 16, 1, lens, True, carry, tail=2)
+
+
+# ------------------- what a call has no business to read or write ----------------
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [50, 700])
+def test_bad_offsets_read_and_write_nothing_outside(dtype, rows):
+    """Every input between NaN bands and every output between canaries, offsets that
+    descend, are negative or point behind the rows: all that is there stays finite.
+    700 rows: scans that are cut."""
+    dtype, d, s = TYPES[dtype], 16, 16
+    assert (chunk_tokens(3, rows, d, s, packed=True) is not None) == (rows == 700)
+    normal = draws(41)
+    torch.manual_seed(41)
+    t = scan_inputs(normal, (rows,), d, s, 1, dtype)
+    w, bias = normal(d, 4, dtype=dtype), normal(d, dtype=dtype)
+    first = [normal(3, 3, d, dtype=dtype), normal(3, d, s)]
+    guards = {}
+    for name, v in t.items():
+        guards[name], t[name] = guarded_input(v.contiguous())
+    guards["w"], w = guarded_input(w)
+    guards["bias"], bias = guarded_input(bias)
+    for offsets in ([0, 40, 20, 50], [-5, 10, 900, 50], [60, 70, 80, 90], [50, 30, 10, 0], [-9, -8, -7, -6],
+                    [0, rows, rows // 3, rows], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -2 ** 31], [-2 ** 31, 2 ** 31 - 1, 0, 5]):
+        guards["offsets"], off = guarded_input(torch.tensor(offsets, dtype=torch.int32).cuda())
+        for carry in (False, True):
+            def buffers(like):
+                g_out, g_state = Guarded(rows * d * t["x"].element_size(), "cuda"), Guarded(like.numel() * like.element_size(), "cuda")
+                out, state = g_out.tensor((rows, d), dtype), g_state.tensor(tuple(like.shape), like.dtype)
+                out.fill_(7.0)
+                state.copy_(like)
+                return g_out, g_state, out, state
+            made = [buffers(like) for like in first]
+            dc.conv1d_causal(t["x"], w, bias, "silu", offsets=off, state=made[0][3], carry=carry, out=made[0][2])
+            dc.selective_scan(**t, softplus=True, offsets=off, state=made[1][3], carry=carry, out=made[1][2])
+            torch.cuda.synchronize()
+            for what, (g_out, g_state, out, state) in zip(("conv", "scan"), made):
+                g_out.assert_intact(f"{what} out {offsets}")
+                g_state.assert_intact(f"{what} state {offsets}")
+                assert out.isfinite().all() and state.isfinite().all(), (what, offsets)
+            for name, guard in guards.items():
+                guard.assert_intact(name)
