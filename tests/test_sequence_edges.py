@@ -322,3 +322,24 @@ def test_bad_offsets_read_and_write_nothing_outside(dtype, rows):
                 assert out.isfinite().all() and state.isfinite().all(), (what, offsets)
             for name, guard in guards.items():
                 guard.assert_intact(name)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("carry", [False, True])
+def test_windows_of_other_slots_keep_their_values(dtype, carry):
+    """Prompts and steps into scattered slots, one left out: every other window is the same to the bit."""
+    normal, dtype = draws(43), TYPES[dtype]
+    lens, slots = [5, 40, 3, 0, 7, 33], [8, 0, -1, 3, 99, 5]
+    x, w = normal(sum(lens), 32, dtype=dtype), normal(32, 4, dtype=dtype)
+    offsets = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32).cuda()
+    where = torch.tensor(slots, dtype=torch.int32).cuda()
+    before = normal(10, 3, 32, dtype=dtype)
+    others = [i for i in range(10) if i not in slots]
+    state = before.clone()
+    dc.conv1d_causal(x, w, offsets=offsets, state=state, slots=where, carry=carry)
+    assert torch.equal(state[others], before[others]) and not torch.equal(state[[8, 0, 5]], before[[8, 0, 5]])
+    assert torch.equal(state[3], before[3] if carry else torch.zeros_like(before[3]))
+    state = before.clone()
+    dc.conv1d_causal_step(x[:6], w, state, slots=where)
+    assert torch.equal(state[others], before[others]) and torch.equal(state[[8, 0, 3, 5], 2], x[[0, 1, 3, 5]])
