@@ -13,10 +13,12 @@
 // ring of eight in shared memory that each thread fills for itself with cp.async:
 // the bytes in flight then cost no registers, of which the taps and the window
 // (2K - 1 values a channel) already take most.  4 x 4096 rows of 4096 bf16 channels,
-// K = 4, silu: 51 us = 5.3 TB/s, 81 % of the copy rate; with the rows in flight held
+// K = 4, silu: 50 us = 5.4 TB/s, 82 % of the copy rate; with the rows in flight held
 // in registers (8 at a time, twice) 64 us, without any in flight while the others
 // are worked on 91 us.  Two or four rows worked on together, eight channel bytes a
 // thread, or registers capped for more blocks an SM: 52 to 120 us.
+// Where 16-byte accesses are not possible a thread owns one channel: 4096 rows of 4092
+// bf16 channels 26 us, 2.6 TB/s.
 #include <cuda_runtime.h>
 
 #include "sequence.cuh"
@@ -385,7 +387,9 @@ cudaError_t launch(void (*kernel)(const Args), const Args& p, int groups, long l
   return cudaGetLastError();
 }
 
-constexpr long long kFullThreads = 148 * 324;   // threads that fill the device
+// Threads below which walks are made shorter: a little under the 51200 of 5120 rows of
+// 1280 fp16 channels in walks of 16, the fastest there.  No other sizes were swept.
+constexpr long long kFullThreads = 148 * 324;
 
 template <typename T, int K>
 cudaError_t conv_typed(ConvArgs p, cudaStream_t s) {

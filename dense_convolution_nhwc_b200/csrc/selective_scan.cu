@@ -18,7 +18,7 @@
 //    lane (of 16) read b, c and delta a quarter as often as one would.
 //  * Two tokens' arguments, additions and sums are one packed instruction each; only
 //    the h chain itself is sequential.  A tile of 32 tokens is one straight piece of
-//    code (in pieces of 16: 334 us, of 8: 366 us, against 309 us).
+//    code (in pieces of 16: 334 us, of 8: 366 us, when this took 309).
 //  * The sums over a channel's lanes are taken for 8 tokens together, so that each lane
 //    ends with its own tokens' sums (24 instructions for 8 tokens, not 6 for each).
 //  * The rest is done by other warps beside the scanning ones: a helping thread owns one
@@ -27,15 +27,15 @@
 //    scanners are at this one.  Done by the scanning warps themselves between their
 //    tiles, the call took 393 us.  b becomes fp32 pairs on the way, c stays as it comes:
 //    both in fp32 the shared-memory reads bound the kernel, neither the conversions do.
-// 8192 tokens of 4096 bf16 channels: 309 us (47 % of the special functions' rate; one block an
-// SM, bound by the latency of one scanning warp a scheduler: 72 clocks a token).  16
-// sequences of 512 tokens: 239 us (60 %).
+// 8192 tokens of 4096 bf16 channels: 311 us (46 % of the special functions' rate; 128 blocks
+// on 148 SMs, bound by the latency of one scanning warp a scheduler: 75 clocks a token).
+// 16 sequences of 512 tokens: 240 us (60 %).
 //
 // A call with too few channels to fill the device cuts the sequences into chunks: a
 // first launch leaves each chunk's final state from zero and its sum of delta in the
 // workspace, and every chunk of the second folds those before it into its first state
 // (the decay over a chunk is exp(a sum delta), see fold).  That doubles the exponentials.  16384
-// tokens of 96 fp32 channels: 35 us.
+// tokens of 96 fp32 channels: 36 us.
 #include <cuda_runtime.h>
 
 #include "sequence.cuh"
@@ -63,7 +63,10 @@ struct ScanArgs {
 // Copies tiles of kRows x cols elements (cols <= kCols) of a tensor's consecutive
 // rows into shared rows kCols elements apart, by kN threads of which this is `me`.
 // `bytes`: an access (16, 8, 4, or 0 for single elements), cols and every address
-// multiples of it.  The 16-byte form keeps each thread's address from tile to tile.
+// multiples of it.  In the 16-byte form each thread keeps its address from tile to tile
+// where a tile's rows are a multiple of those that the threads cover together (kFits:
+// fp32 with 16 states, say; with 16-bit types they cover 64 rows and the addresses are
+// worked out anew).
 template <typename T, int kRows, int kCols, int kN>
 struct Stager {
   static constexpr int E = 16 / sizeof(T), kPer = kCols / E > 0 ? kCols / E : 1;
@@ -970,7 +973,7 @@ ScanPlan plan_scan(const selective_scan_desc_t& d, int sm_count) {
   plan.chunk = d.l > 0 ? (d.l + kTile - 1) / kTile * kTile : kTile;
   plan.chunks = 1;
   // Cut, every token is gone over twice: it pays from four chunks on (8192 tokens of
-  // 2048 channels, 4 chunks: 242 us against 322; 2048 of 3000, 3 chunks: 89 against 84).
+  // 2048 channels, 4 chunks: 236 us against 322; 2048 of 3000, 3 chunks: 89 against 84).
   // Two blocks an SM are enough, and a chunk's start is worked out from all chunks
   // before it, so not too many (16384 tokens of 32 channels: 27.5 us in 148 chunks,
   // 38.6 in 256) nor too short ones.

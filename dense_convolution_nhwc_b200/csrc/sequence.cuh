@@ -140,6 +140,7 @@ __device__ __forceinline__ float lowest(const float (&v)[V], float so_far) {
 // case), so log1p(t) = 2 artanh(s), s = t / (2 + t) <= 1/3, and artanh(s) / s is a
 // polynomial in s^2, fitted over [0, 1/9] for the least largest relative error
 // (8e-9 with its coefficients in fp32; its Taylor series takes three terms more).
+// Results below 2^-126 (v < -87.3) are zero.
 __device__ __forceinline__ float2 softplus(float2 v) {
   const float2 t = make_float2(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
   const float2 low = __fadd2_rn(t, make_float2(2.0f, 2.0f));

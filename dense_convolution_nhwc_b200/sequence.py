@@ -127,7 +127,8 @@ def _enqueue(call, index, *args):
 def conv1d_causal(x, w, bias=None, activation=None, offsets=None, state=None, slots=None, carry=False, out=None):
     """Short depthwise causal conv1d over prompts, w [C, K] with 2 <= K <= 8, the last
     tap on the token itself: x [N, L, C], or packed [T, C] with int32 offsets [n + 1]
-    (rows outside every sequence are left as they are).  The K-1 tokens before a
+    (rows outside every sequence, or of one whose slot is outside the cache, are left
+    as they are: whatever memory held, where out is not given).  The K-1 tokens before a
     sequence are zero, or with carry its slot of state [slots, K-1, C]; the last K-1
     tokens are left in state where one is given.  x may be a slice of wider rows."""
     packed = offsets is not None
@@ -151,7 +152,8 @@ def conv1d_causal(x, w, bias=None, activation=None, offsets=None, state=None, sl
 def conv1d_causal_step(x, w, state, bias=None, activation=None, slots=None, out=None):
     """conv1d_causal for one new token of each of N sequences: x [N, C], the window of
     sequence i in slot i, or slots[i], of state [slots, K-1, C], shifted in place.  A
-    sequence whose slot is outside the cache (-1) is left out, its row of out too."""
+    sequence whose slot is outside the cache (-1) is left out, its row of out too (which
+    holds whatever memory held, where out is not given)."""
     code, index, shape, dtype = _input(x, 2)
     (n, c), k = shape, _filter(w)
     xp, xs = _rows(x, "x", shape, dtype, index)
@@ -190,8 +192,9 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=False,
     delta_t = dt_t + dt_bias, through log(1 + exp(.)) with softplus.
 
     x, dt, z [N, L, D], b, c [N, L, G, S], or packed [T, D], [T, G, S] with int32 offsets
-    [n + 1] (rows outside every sequence are left as they are); a [D, S], d, dt_bias [D]
-    in fp32.  h starts from zero, or with carry from state [slots, D, S] (fp32), and is
+    [n + 1] (rows outside every sequence, or of one whose slot is outside the cache, are
+    left as they are: whatever memory held, where out is not given); a [D, S], d, dt_bias
+    [D] in fp32.  h starts from zero, or with carry from state [slots, D, S] (fp32), and is
     left there where one is given.  x, dt, z, b, c may be slices of wider rows."""
     packed = offsets is not None
     code, index, shape, dtype = _input(x, 2 if packed else 3)
@@ -233,7 +236,7 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, sof
     """selective_scan for one new token of each of N sequences: x, dt, z [N, D], b, c
     [N, G, S], the state of sequence i in slot i, or slots[i], of state [slots, D, S]
     (fp32), advanced in place.  A sequence whose slot is outside the cache (-1) is left
-    out, its row of out too."""
+    out, its row of out too (which holds whatever memory held, where out is not given)."""
     code, index, shape, dtype = _input(x, 2)
     n, dim = shape
     g, s = _groups(b, 2, dim)

@@ -253,7 +253,11 @@ B200CONV_API conv_status_t conv1d_forward(const void *in, const void *w, void *o
  *    overlap each other or any input (CONV_ERR_INVALID); the spans between a
  *    tensor's first and last element are compared.
  * Inputs and out are of `dtype` (weights and bias of the convolution too);
- * arithmetic and the scan's state are fp32, each output rounded once.
+ * arithmetic and the scan's state are fp32, each output rounded once.  A token's
+ * delta and decay exp(delta * a) are fp32 values, and zero below 2^-126: an infinite
+ * state times such a decay is NaN.  A long scan may be carried over many tokens
+ * at once.  The product of their decays may leave fp32's range; what a state before
+ * them and their own inputs give after them may not, even where the two cancel.
  */
 typedef enum { CONV_ACT_NONE = 0, CONV_ACT_SILU = 1 /* v / (1 + exp(-v)) */ } conv_activation_t;
 
